@@ -59,6 +59,11 @@ enum tq_status {
 #define TQ_DEV_SLOT_RANGE   0x1u  /* slot_mapping entry beyond the cache; token skipped  */
 #define TQ_DEV_BLOCK_RANGE  0x2u  /* block_table entry beyond the cache; page skipped    */
 #define TQ_DEV_WAIT_TIMEOUT 0x4u  /* a bounded on-chip wait gave up; results invalid    */
+#define TQ_DEV_ROW          0x8u  /* a row out of range, named twice, in use, or with an impossible length, or
+                                     an output too short for it; its request skipped     */
+#define TQ_DEV_NO_PAGES     0x10u /* no free pages left, or a table row too short; request skipped */
+#define TQ_DEV_PAGE_SHARED  0x20u /* tokens would go into a page that another row reads; request skipped */
+#define TQ_DEV_KEEP_RANGE   0x40u /* a kept token outside its row; request skipped       */
 
 /* Input dtypes for tq_encode. */
 #define TQ_DTYPE_BF16 0
@@ -312,6 +317,122 @@ size_t tq_score_workspace_bytes(const tq_cache_desc *desc, int64_t n_db, int n_q
 int tq_score(const tq_params *p, const tq_cache_desc *desc, const void *db_cache, int64_t n_db,
              const float *Q, int n_q, int k, float *top_scores, int64_t *top_idx,
              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Pages of a cache: reserving, forking, compacting, freeing                 */
+/* ------------------------------------------------------------------------ */
+/* The block table of a cache kept on the device.  Row r of table holds the
+ * pages of one sequence, lens[r] its tokens (0: the row is empty); refs[b]
+ * counts the rows that list page b, 0 = free.  The caller owns the three
+ * arrays (zero lens and refs: an empty pool) and only these calls change
+ * refs.  One table serves all layers of a model: every layer's cache has the
+ * same shape and the same page numbers.
+ *
+ * All four calls run on the stream without the host seeing anything, so they
+ * can be captured; calls on one pool are ordered by the stream.  Free pages
+ * are dealt lowest number first, in the order of the requests; once they run
+ * out, that request and the later ones that need pages are skipped.  A
+ * request that cannot be served changes nothing and sets a TQ_DEV_* bit in the
+ * workspace's status word (TQ_DEV_BLOCK_RANGE: its row lists a page that is
+ * out of range or free).  Entries of a table row behind its pages are never
+ * read, and stay as they were.  num_blocks * page_tokens and
+ * max_blocks * page_tokens fit 31 bits.
+ * workspace: >= tq_pages_workspace_bytes(num_blocks, n_rows, max_blocks),
+ * 256-byte aligned. */
+typedef struct {
+    int32_t *refs;        /* device [num_blocks]          */
+    int32_t *table;       /* device [n_rows][max_blocks]  */
+    int32_t *lens;        /* device [n_rows]              */
+    int64_t num_blocks;   /* >= 1                         */
+    int n_rows;           /* >= 1                         */
+    int max_blocks;       /* >= 1                         */
+} tq_page_pool;
+
+size_t tq_pages_workspace_bytes(int64_t num_blocks, int n_rows, int max_blocks);
+
+/* Room for new_tokens[r] (device [n_rows]; <= 0: none) more tokens of every
+ * row r: pages where its last one is full, lens[r] += new_tokens[r], and in
+ * slot_mapping (device [n_slots], what tq_encode and tq_decode_step take) the
+ * slots of row 0's tokens, then row 1's, and so on; -1 for the tokens of a
+ * skipped row and for entries behind the last token. */
+int tq_pages_reserve(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *new_tokens,
+                     int32_t *slot_mapping, int64_t n_slots, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Row dst_rows[i] (empty) becomes a copy of row src_rows[i] (device arrays of
+ * n <= n_rows): full pages are shared, a partly filled last page is copied
+ * whole into a fresh page in each of the n_layers caches (host array of
+ * device pointers).  A row may be forked many times; a dst row named twice is
+ * served once, for the first. */
+int tq_pages_fork(const tq_cache_desc *desc, const tq_page_pool *pool, void *const *caches, int n_layers,
+                  const int32_t *src_rows, const int32_t *dst_rows, int n, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* Row rows[i] keeps only the tokens keep[i][0 .. keep_lens[i]) (device
+ * [n][keep_stride], positions of the row as it was, in any order, any number
+ * of times), which become its positions 0, 1, ...: their records are gathered
+ * into fresh pages in each layer, and the pages they leave are released.  A
+ * page whose positions all keep their own token stays as it is (shared, too)
+ * if it is full or this row's alone; so dropping the last tokens moves at
+ * most one page.  Slots of a fresh page behind the last token are not
+ * written.  The fresh pages are taken before the old ones are released. */
+int tq_pages_compact(const tq_cache_desc *desc, const tq_page_pool *pool, void *const *caches, int n_layers,
+                     const int32_t *rows, const int32_t *keep, int keep_stride, const int32_t *keep_lens, int n,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rows rows[0 .. n) give their pages back and become empty (an empty row, or
+ * one named twice, gives nothing more). */
+int tq_pages_free(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *rows, int n, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Head norms with rotary positions                                         */
+/* ------------------------------------------------------------------------ */
+/* Which two coordinates form pair p (0 <= p < rot_dim / 2). */
+#define TQ_ROPE_HALF 0    /* (p, p + rot_dim / 2) */
+#define TQ_ROPE_PAIRS 1   /* (2 p, 2 p + 1)       */
+
+/* The position rotation of one head.  Pair p turns by the angle
+ * pos[pair_axis[p]] * inv_freq[p]; coordinates rot_dim .. d-1 do not turn.
+ * One axis is the position in a text; several axes are the positions of an
+ * image or video token (time, height, width), each pair following one. */
+typedef struct {
+    int d;                    /* head dimension, even, 2..256                   */
+    int rot_dim;              /* rotated coordinates, even, 0..d                */
+    int style;                /* TQ_ROPE_*                                      */
+    int n_axes;               /* 1..8                                           */
+    float eps;                /* of the norm, >= 0                              */
+    float scale;              /* multiplies the rotated coordinates (1: none)   */
+    uint8_t pair_axis[128];   /* axis of each pair, < n_axes (host memory)      */
+} tq_rope_desc;
+
+/* The heads of one tensor: vector (t, h) starts at x + t * tok_stride +
+ * h * head_stride elements and its d coordinates are adjacent; the result
+ * goes to out with its own strides.  weight: [d], or NULL for no norm.  out
+ * may be x itself with the same strides; otherwise the two do not overlap,
+ * and neither do the vectors of out.  Every pointer is aligned to its
+ * element. */
+typedef struct {
+    const void *x;
+    int64_t tok_stride, head_stride;
+    const void *weight;
+    void *out;
+    int64_t out_tok_stride, out_head_stride;
+    int n_heads;
+} tq_heads;
+
+/* For every token t and head of q and k (either may be NULL):
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (y = x without a weight)
+ *   (a, b) = pair p of y -> scale (a cos u - b sin u, b cos u + a sin u),
+ *   u = positions[pair_axis[p] * axis_stride + t] * inv_freq[p],
+ * what an attention layer does to the slices of its QKV projection before
+ * tq_encode and the attention calls.  dtype / w_dtype: TQ_DTYPE_* of x, out /
+ * of the weights.  Sums are fp32, angles fp64 until they are reduced to one
+ * turn (far positions keep their phase), the result is rounded once.
+ * positions: device int32, any sign; inv_freq: device fp32 [rot_dim / 2].
+ * Asynchronous; no workspace. */
+int tq_qk_norm_rope(const tq_rope_desc *desc, int dtype, int w_dtype, int64_t n_tokens, const tq_heads *q,
+                    const tq_heads *k, const int32_t *positions, int64_t axis_stride, const float *inv_freq,
+                    void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                   */

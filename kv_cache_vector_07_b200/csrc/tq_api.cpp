@@ -235,6 +235,115 @@ extern "C" int tq_score(const tq_params *p, const tq_cache_desc *desc, const voi
                                         top_idx, static_cast<uint8_t *>(workspace), workspace_bytes, stream));
 }
 
+namespace {
+
+bool heads_ok(const tq_heads *h, int64_t n, int es, int wes) {
+    if (!h) return true;
+    if (h->n_heads < 1 || h->n_heads > 65535) return false;
+    if (n == 0) return true;
+    return h->x && h->out && aligned(h->x, es) && aligned(h->out, es) && aligned(h->weight, wes);
+}
+
+}  // namespace
+
+extern "C" int tq_qk_norm_rope(const tq_rope_desc *desc, int dtype, int w_dtype, int64_t n_tokens, const tq_heads *q,
+                               const tq_heads *k, const int32_t *positions, int64_t axis_stride,
+                               const float *inv_freq, void *stream) {
+    if (!desc || (!q && !k) || n_tokens < 0) return TQ_EINVAL;
+    if (desc->d < 2 || desc->d > 256 || (desc->d & 1)) return TQ_EUNSUPPORTED;
+    if (desc->rot_dim < 0 || desc->rot_dim > desc->d || (desc->rot_dim & 1)) return TQ_EINVAL;
+    if (desc->style != TQ_ROPE_HALF && desc->style != TQ_ROPE_PAIRS) return TQ_EINVAL;
+    if (desc->n_axes < 1 || desc->n_axes > 8 || !(desc->eps >= 0.f)) return TQ_EINVAL;
+    for (int p = 0; p < desc->rot_dim / 2; ++p)
+        if (desc->pair_axis[p] >= desc->n_axes) return TQ_EINVAL;
+    if (dtype != TQ_DTYPE_BF16 && dtype != TQ_DTYPE_F32) return TQ_EINVAL;
+    if (w_dtype != TQ_DTYPE_BF16 && w_dtype != TQ_DTYPE_F32) return TQ_EINVAL;
+    const int es = dtype == TQ_DTYPE_F32 ? 4 : 2, wes = w_dtype == TQ_DTYPE_F32 ? 4 : 2;
+    if (!heads_ok(q, n_tokens, es, wes) || !heads_ok(k, n_tokens, es, wes)) return TQ_EINVAL;
+    if (n_tokens == 0) return TQ_OK;
+    if (desc->rot_dim > 0 && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 4)))
+        return TQ_EINVAL;
+    if (desc->rot_dim > 0 && desc->n_axes > 1 && axis_stride < n_tokens) return TQ_EINVAL;
+    return cuda_status(tq::launch_rope(*desc, dtype, w_dtype, n_tokens, q, k, positions, axis_stride, inv_freq,
+                                       stream));
+}
+
+extern "C" size_t tq_pages_workspace_bytes(int64_t num_blocks, int n_rows, int max_blocks) {
+    if (num_blocks < 1 || num_blocks > INT32_MAX || n_rows < 1 || max_blocks < 1) return 0;
+    return tq::pages_ws_bytes(num_blocks, n_rows, max_blocks);
+}
+
+namespace {
+
+bool pool_ok(const tq_cache_desc *desc, const tq_page_pool *p, void *ws, size_t ws_bytes) {
+    if (!valid_desc(desc) || !p || !ws || !aligned(ws, 256)) return false;
+    if (!p->refs || !p->table || !p->lens) return false;
+    if (!aligned(p->refs, 4) || !aligned(p->table, 4) || !aligned(p->lens, 4)) return false;
+    if (p->num_blocks < 1 || p->n_rows < 1 || p->max_blocks < 1) return false;
+    if (p->num_blocks > INT32_MAX / desc->page_tokens || p->max_blocks > INT32_MAX / desc->page_tokens) return false;
+    return ws_bytes >= tq::pages_ws_bytes(p->num_blocks, p->n_rows, p->max_blocks);
+}
+
+bool layers_ok(void *const *caches, int n_layers) {
+    if (!caches || n_layers < 1) return false;
+    for (int i = 0; i < n_layers; ++i)
+        if (!caches[i] || !aligned(caches[i], 256)) return false;
+    return true;
+}
+
+bool ints_ok(const int32_t *p) { return p && aligned(p, 4); }
+
+}  // namespace
+
+extern "C" int tq_pages_reserve(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *new_tokens,
+                                int32_t *slot_mapping, int64_t n_slots, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    if (!pool_ok(desc, pool, workspace, workspace_bytes) || !ints_ok(new_tokens) || n_slots < 0) return TQ_EINVAL;
+    if (n_slots > 0 && !ints_ok(slot_mapping)) return TQ_EINVAL;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    return cuda_status(tq::launch_pages_reserve(L, *pool, new_tokens, slot_mapping, n_slots,
+                                                static_cast<uint8_t *>(workspace), stream));
+}
+
+extern "C" int tq_pages_fork(const tq_cache_desc *desc, const tq_page_pool *pool, void *const *caches, int n_layers,
+                             const int32_t *src_rows, const int32_t *dst_rows, int n, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    if (!pool_ok(desc, pool, workspace, workspace_bytes) || !layers_ok(caches, n_layers)) return TQ_EINVAL;
+    if (n < 0 || n > pool->n_rows) return TQ_EINVAL;
+    if (n == 0) return TQ_OK;
+    if (!ints_ok(src_rows) || !ints_ok(dst_rows)) return TQ_EINVAL;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    return cuda_status(tq::launch_pages_fork(L, *pool, caches, n_layers, src_rows, dst_rows, n,
+                                             static_cast<uint8_t *>(workspace), stream));
+}
+
+extern "C" int tq_pages_compact(const tq_cache_desc *desc, const tq_page_pool *pool, void *const *caches,
+                                int n_layers, const int32_t *rows, const int32_t *keep, int keep_stride,
+                                const int32_t *keep_lens, int n, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    if (!pool_ok(desc, pool, workspace, workspace_bytes) || !layers_ok(caches, n_layers)) return TQ_EINVAL;
+    if (n < 0 || n > pool->n_rows || keep_stride < 0) return TQ_EINVAL;
+    if (n == 0) return TQ_OK;
+    if (!ints_ok(rows) || !ints_ok(keep_lens) || (keep_stride > 0 && !ints_ok(keep))) return TQ_EINVAL;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    return cuda_status(tq::launch_pages_compact(L, *pool, caches, n_layers, rows, keep, keep_stride, keep_lens, n,
+                                                static_cast<uint8_t *>(workspace), stream));
+}
+
+extern "C" int tq_pages_free(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *rows, int n,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool_ok(desc, pool, workspace, workspace_bytes)) return TQ_EINVAL;
+    if (n < 0) return TQ_EINVAL;
+    if (n == 0) return TQ_OK;
+    if (!ints_ok(rows)) return TQ_EINVAL;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    return cuda_status(tq::launch_pages_free(L, *pool, rows, n, static_cast<uint8_t *>(workspace), stream));
+}
+
 extern "C" int tq_read_status(void *workspace, void *stream, uint32_t *flags) {
     if (!workspace || !flags) return TQ_EINVAL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -226,6 +226,22 @@ int launch_pf128(const tq_params *kp, const tq_params *vp, const Layout &L, cons
                  const AttnShape &s, int n_splits, int split_len, const uint8_t *cache, int64_t num_blocks,
                  float *part_o, float *part_ml, uint32_t *status, cudaStream_t st);
 
+// Head norms with rotary positions (arguments checked by the caller).
+int launch_rope(const tq_rope_desc &rd, int dtype, int w_dtype, int64_t n, const tq_heads *q, const tq_heads *k,
+                const int32_t *positions, int64_t axis_stride, const float *inv_freq, void *stream);
+
+// Pages of a cache (arguments checked by the caller).
+size_t pages_ws_bytes(int64_t num_blocks, int n_rows, int max_blocks);
+int launch_pages_reserve(const Layout &L, const tq_page_pool &pool, const int32_t *new_tokens, int32_t *slots,
+                         int64_t n_slots, uint8_t *ws, void *stream);
+int launch_pages_fork(const Layout &L, const tq_page_pool &pool, void *const *caches, int n_layers,
+                      const int32_t *src, const int32_t *dst, int n, uint8_t *ws, void *stream);
+int launch_pages_compact(const Layout &L, const tq_page_pool &pool, void *const *caches, int n_layers,
+                         const int32_t *rows, const int32_t *keep, int keep_stride, const int32_t *keep_lens, int n,
+                         uint8_t *ws, void *stream);
+int launch_pages_free(const Layout &L, const tq_page_pool &pool, const int32_t *rows, int n, uint8_t *ws,
+                      void *stream);
+
 size_t score_ws_bytes(const Layout &L, int64_t n_db, int n_q, int k);
 // Tensor-core search (4-bit + QJL database, d in {128, 256, 512, 1024},
 // k <= 16): blocks per query tile, or 0 when not covered; workspace pieces;

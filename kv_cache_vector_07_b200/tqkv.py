@@ -29,8 +29,10 @@ _lib = ctypes.CDLL(LIB_PATH)
 TQ_OK, TQ_EINVAL, TQ_EUNSUPPORTED, TQ_ECUDA, TQ_EDEVICE, TQ_ENOMEM, TQ_ESCRATCH = range(7)
 TQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 TQ_DEV_SLOT_RANGE, TQ_DEV_BLOCK_RANGE, TQ_DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+TQ_DEV_ROW, TQ_DEV_NO_PAGES, TQ_DEV_PAGE_SHARED, TQ_DEV_KEEP_RANGE = 0x8, 0x10, 0x20, 0x40
 TQ_DTYPE_BF16, TQ_DTYPE_F32 = 0, 1
 TQ_ROT_HADAMARD, TQ_ROT_DENSE = 0, 1
+TQ_ROPE_HALF, TQ_ROPE_PAIRS = 0, 1
 TQ_BITS_HALF = 16
 TQ_BITS_POLAR = 32
 
@@ -67,6 +69,24 @@ class CacheDesc(ctypes.Structure):
                 f"page_tokens={self.page_tokens}, n_kv_heads={self.n_kv_heads})")
 
 
+class RopeDesc(ctypes.Structure):
+    """Mirror of tq_rope_desc."""
+    _fields_ = [("d", _i32), ("rot_dim", _i32), ("style", _i32), ("n_axes", _i32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("pair_axis", ctypes.c_uint8 * 128)]
+
+
+class _Heads(ctypes.Structure):
+    """Mirror of tq_heads."""
+    _fields_ = [("x", _vp), ("tok_stride", _i64), ("head_stride", _i64), ("weight", _vp), ("out", _vp),
+                ("out_tok_stride", _i64), ("out_head_stride", _i64), ("n_heads", _i32)]
+
+
+class _PagePool(ctypes.Structure):
+    """Mirror of tq_page_pool."""
+    _fields_ = [("refs", _vp), ("table", _vp), ("lens", _vp), ("num_blocks", _i64), ("n_rows", _i32),
+                ("max_blocks", _i32)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -97,6 +117,14 @@ _sig("tq_prefill_attn", _i32, [_vp, _vp, ctypes.POINTER(CacheDesc), _vp, _i32, _
                                _vp, _vp, _vp, _sz, _vp])
 _sig("tq_score_workspace_bytes", _sz, [ctypes.POINTER(CacheDesc), _i64, _i32, _i32])
 _sig("tq_score", _i32, [_vp, ctypes.POINTER(CacheDesc), _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
+_pool_p, _desc_p, _ptrs = ctypes.POINTER(_PagePool), ctypes.POINTER(CacheDesc), ctypes.POINTER(_vp)
+_sig("tq_pages_workspace_bytes", _sz, [_i64, _i32, _i32])
+_sig("tq_pages_reserve", _i32, [_desc_p, _pool_p, _vp, _vp, _i64, _vp, _sz, _vp])
+_sig("tq_pages_fork", _i32, [_desc_p, _pool_p, _ptrs, _i32, _vp, _vp, _i32, _vp, _sz, _vp])
+_sig("tq_pages_compact", _i32, [_desc_p, _pool_p, _ptrs, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _sz, _vp])
+_sig("tq_pages_free", _i32, [_desc_p, _pool_p, _vp, _i32, _vp, _sz, _vp])
+_sig("tq_qk_norm_rope", _i32, [ctypes.POINTER(RopeDesc), _i32, _i32, _i64, ctypes.POINTER(_Heads),
+                               ctypes.POINTER(_Heads), _vp, _i64, _vp, _vp])
 _sig("tq_read_status", _i32, [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)])
 _sig("tq_status_string", ctypes.c_char_p, [_i32])
 _sig("tq_test_stall_next_decode", _i32, [ctypes.c_uint32])
@@ -150,6 +178,29 @@ def _dev_check(*tensors):
     for t in tensors:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("libtqkv arguments must be contiguous CUDA tensors")
+
+
+def _same_device(*tensors) -> int:
+    """The index of the one CUDA device that all given tensors are on."""
+    at = {t.device for t in tensors if t is not None}
+    if len(at) != 1 or next(iter(at)).type != "cuda":
+        raise ValueError("libtqkv arguments must be CUDA tensors of one device")
+    return next(iter(at)).index
+
+
+class _on:
+    """The given device made current for a call, where it is not already."""
+
+    def __init__(self, index: int):
+        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
 
 
 # ---------------------------------------------------------------------------
@@ -377,6 +428,164 @@ def score(p: Params, desc: CacheDesc, db_cache: torch.Tensor, n_db: int, Q: torc
     _check(_lib.tq_score(p.handle, ctypes.byref(desc), _ptr(db_cache), n_db, _ptr(Q), n_q, k, _ptr(top_scores),
                          _ptr(top_idx), _ptr(workspace), workspace.numel(), _stream(stream)), "tq_score")
     return top_scores, top_idx
+
+
+# ---------------------------------------------------------------------------
+# pages of a cache
+# ---------------------------------------------------------------------------
+def pages_workspace_bytes(num_blocks: int, n_rows: int, max_blocks: int) -> int:
+    return int(_lib.tq_pages_workspace_bytes(num_blocks, n_rows, max_blocks))
+
+
+def _pool(desc, refs, table, lens, caches, ints, workspace):
+    """(device index, tq_page_pool, cache pointers, workspace) of a pages call."""
+    layers = () if caches is None else [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    dev = _same_device(refs, table, lens, workspace, *ints, *layers)
+    if refs.dim() != 1 or table.dim() != 2 or lens.shape != table.shape[:1]:
+        raise ValueError("refs must be [num_blocks], table [n_rows, max_blocks] and lens [n_rows]")
+    for t in (refs, table, lens, *ints):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("refs, table, lens and the requests must be contiguous int32 tensors")
+    if caches is not None and not layers:
+        raise ValueError("caches must name one cache at least")
+    for c in layers:
+        if c.dtype != torch.uint8 or not c.is_contiguous() or \
+                c.shape != (refs.shape[0], desc.n_kv_heads, cache_bytes(desc)):
+            raise ValueError("every cache must be contiguous uint8 [num_blocks, n_kv_heads, page bytes]")
+    if workspace is None:
+        workspace = _workspace(pages_workspace_bytes(refs.shape[0], *table.shape), refs.device)
+    pool = _PagePool(refs.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.shape[0], *table.shape)
+    return dev, pool, (_vp * len(layers))(*[c.data_ptr() for c in layers]), workspace
+
+
+def pages_reserve(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                  new_tokens: torch.Tensor, slot_mapping: torch.Tensor, workspace: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """tq_pages_reserve: pages and slots for new_tokens int32 [n_rows] more
+    tokens of every row; slot_mapping int32 [n_slots] receives their slots, row
+    after row.  refs int32 [num_blocks], table int32 [n_rows, max_blocks] and
+    lens int32 [n_rows] are updated.  Returns the workspace (read_status)."""
+    dev, pool, _, workspace = _pool(desc, refs, table, lens, None, (new_tokens, slot_mapping), workspace)
+    if new_tokens.shape != lens.shape or slot_mapping.dim() != 1:
+        raise ValueError("new_tokens must be [n_rows] and slot_mapping [n_slots]")
+    with _on(dev):
+        _check(_lib.tq_pages_reserve(ctypes.byref(desc), ctypes.byref(pool), _ptr(new_tokens), _ptr(slot_mapping),
+                                     slot_mapping.numel(), _ptr(workspace), workspace.numel(), _stream(stream)),
+               "tq_pages_reserve")
+    return workspace
+
+
+def pages_fork(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+               src_rows: torch.Tensor, dst_rows: torch.Tensor, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """tq_pages_fork: rows dst_rows (empty) become copies of rows src_rows
+    (int32 [n]); caches: one cache, or a list with every layer's.  Full pages
+    are shared, partly filled ones copied.  Returns the workspace."""
+    dev, pool, ptrs, workspace = _pool(desc, refs, table, lens, caches, (src_rows, dst_rows), workspace)
+    if src_rows.dim() != 1 or src_rows.shape != dst_rows.shape:
+        raise ValueError("src_rows and dst_rows must be [n]")
+    with _on(dev):
+        _check(_lib.tq_pages_fork(ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), _ptr(src_rows),
+                                  _ptr(dst_rows), src_rows.numel(), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "tq_pages_fork")
+    return workspace
+
+
+def pages_compact(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                  rows: torch.Tensor, keep: torch.Tensor, keep_lens: torch.Tensor,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """tq_pages_compact: row rows[i] keeps its tokens keep[i, :keep_lens[i]]
+    (int32 [n], [n, most], [n]), in that order; caches as in pages_fork.
+    Returns the workspace."""
+    dev, pool, ptrs, workspace = _pool(desc, refs, table, lens, caches, (rows, keep, keep_lens), workspace)
+    if rows.dim() != 1 or keep.dim() != 2 or keep.shape[0] != rows.shape[0] or keep_lens.shape != rows.shape:
+        raise ValueError("rows and keep_lens must be [n] and keep [n, most]")
+    with _on(dev):
+        _check(_lib.tq_pages_compact(ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), _ptr(rows), _ptr(keep),
+                                     keep.shape[1], _ptr(keep_lens), rows.numel(), _ptr(workspace),
+                                     workspace.numel(), _stream(stream)), "tq_pages_compact")
+    return workspace
+
+
+def pages_free(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """tq_pages_free: rows (int32 [n]) give their pages back and become empty.
+    Returns the workspace."""
+    dev, pool, _, workspace = _pool(desc, refs, table, lens, None, (rows,), workspace)
+    if rows.dim() != 1:
+        raise ValueError("rows must be [n]")
+    with _on(dev):
+        _check(_lib.tq_pages_free(ctypes.byref(desc), ctypes.byref(pool), _ptr(rows), rows.numel(), _ptr(workspace),
+                                  workspace.numel(), _stream(stream)), "tq_pages_free")
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# head norms with rotary positions
+# ---------------------------------------------------------------------------
+def rope_desc(d: int, rot_dim: int | None = None, style: int = TQ_ROPE_HALF, pair_axis=None, n_axes: int = 1,
+              eps: float = 1e-6, scale: float = 1.0) -> RopeDesc:
+    """The position rotation of one head (tq_rope_desc); pair_axis: the axis of
+    each of the rot_dim / 2 pairs (all 0 when omitted)."""
+    rot = d if rot_dim is None else rot_dim
+    axis = list(pair_axis) if pair_axis is not None else []
+    if len(axis) > 128 or (axis and len(axis) != rot // 2) or any(not 0 <= a < n_axes for a in axis):
+        raise ValueError("pair_axis holds one axis (0 .. n_axes - 1) for each of the rot_dim / 2 pairs")
+    return RopeDesc(d, rot, style, n_axes, eps, scale, (ctypes.c_uint8 * 128)(*axis))
+
+
+_ROPE_DTYPES = {torch.bfloat16: TQ_DTYPE_BF16, torch.float32: TQ_DTYPE_F32}
+
+
+def _heads(x, weight, out, d, n, name):
+    if x is None:
+        return None, None
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    for t, what in ((x, name), (out, name + "_out")):
+        if t.dim() != 3 or t.shape[2] != d or t.shape[0] != n or (d > 1 and t.stride(2) != 1):
+            raise ValueError(f"{what} must be [n_tokens, heads, d] with adjacent coordinates")
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name}_out must have {name}'s shape and dtype")
+    return _Heads(x.data_ptr(), x.stride(0), x.stride(1), _ptr(weight), out.data_ptr(), out.stride(0), out.stride(1),
+                  x.shape[1]), out
+
+
+def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
+                 inv_freq: torch.Tensor, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """tq_qk_norm_rope: RMS norm (where a weight is given) and position rotation
+    of q [n, Hq, d] and k [n, H, d] (bf16 or fp32, strided slices allowed);
+    positions int32 [n] or [n_axes, n], inv_freq fp32 [rot_dim / 2].  Returns
+    (q_out, k_out), contiguous where not given; q_out may be q itself."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    n = x.shape[0]
+    dev = _same_device(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    dt = _ROPE_DTYPES.get(x.dtype)
+    if dt is None or (q is not None and k is not None and q.dtype != k.dtype):
+        raise ValueError("q and k must both be bf16 or both fp32")
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    if any(w.shape != (desc.d,) or not w.is_contiguous() or w.dtype not in _ROPE_DTYPES or w.dtype != weights[0].dtype
+           for w in weights):
+        raise ValueError("weights must be contiguous [d], both bf16 or both fp32")
+    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float32:
+        raise ValueError("positions must be int32 and inv_freq fp32")
+    if positions.shape not in ((n,), (desc.n_axes, n)) or (positions.dim() == 1 and desc.n_axes != 1) or \
+            (n > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be [n_tokens], or [n_axes, n_tokens], with adjacent tokens")
+    if inv_freq.numel() != desc.rot_dim // 2 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous [rot_dim / 2]")
+    hq, q_out = _heads(q, q_weight, q_out, desc.d, n, "q")
+    hk, k_out = _heads(k, k_weight, k_out, desc.d, n, "k")
+    axis_stride = positions.stride(0) if positions.dim() == 2 else n
+    with _on(dev):
+        _check(_lib.tq_qk_norm_rope(ctypes.byref(desc), dt, _ROPE_DTYPES[weights[0].dtype] if weights else dt, n,
+                                    ctypes.byref(hq) if hq is not None else None,
+                                    ctypes.byref(hk) if hk is not None else None, _ptr(positions), axis_stride,
+                                    _ptr(inv_freq), _stream(stream)), "tq_qk_norm_rope")
+    return q_out, k_out
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:
