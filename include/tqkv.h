@@ -319,6 +319,28 @@ int tq_score(const tq_params *p, const tq_cache_desc *desc, const void *db_cache
              void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Cross attention (runs of queries over whole cached sequences)             */
+/* ------------------------------------------------------------------------ */
+/* Sequence b's cache (block_table row b, kv_lens[b] tokens: an encoder's
+ * states, written once) is read by the queries cu_q[b] .. cu_q[b+1] - 1 (at
+ * most max_q of them), each seeing all of it; the two lengths have nothing to
+ * do with one another.  Q: device bf16 [total_q][Hq][d]; cu_q: device int32
+ * [B + 1], ascending from 0; out: device bf16 [total_q][Hq][d]; lse optional
+ * fp32 [total_q][Hq].  Logits as tq_decode_attn.  A sequence with no tokens
+ * gives zeros (lse -inf); a query with a coordinate that is not finite gives
+ * NaN in its own row and head.  Rows of Q behind cu_q[B], and queries behind a
+ * run's first max_q (TQ_DEV_ROW), are neither read nor written.  kv_lens above
+ * max_kv_len count as max_kv_len.  Keys of a page out of range are left out
+ * (TQ_DEV_BLOCK_RANGE).
+ * workspace: >= tq_cross_workspace_bytes(desc, B, total_q, max_q, Hq,
+ * max_kv_len), 256-byte aligned. */
+size_t tq_cross_workspace_bytes(const tq_cache_desc *desc, int B, int total_q, int max_q, int Hq, int max_kv_len);
+int tq_cross_attn(const tq_params *kp, const tq_params *vp, const tq_cache_desc *desc, const void *Q, int total_q,
+                  int max_q, int Hq, const int32_t *cu_q, int B, const int32_t *block_table, int max_blocks,
+                  const int32_t *kv_lens, int max_kv_len, const void *cache, int64_t num_blocks, void *out, float *lse,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Pages of a cache: reserving, forking, compacting, freeing                 */
 /* ------------------------------------------------------------------------ */
 /* The block table of a cache kept on the device.  Row r of table holds the

@@ -268,6 +268,69 @@ extern "C" int tq_qk_norm_rope(const tq_rope_desc *desc, int dtype, int w_dtype,
                                        stream));
 }
 
+namespace {
+
+tq::CrossShape cross_shape(int B, int total_q, int max_q, int Hq, int max_kv_len) {
+    tq::CrossShape s{};
+    s.B = B;
+    s.total_q = total_q;
+    s.max_q = max_q < total_q ? max_q : total_q;
+    s.Hq = Hq;
+    s.max_kv_len = max_kv_len;
+    return s;
+}
+
+bool cross_sizes_ok(const tq_cache_desc *desc, int B, int total_q, int max_q, int Hq, int max_kv_len) {
+    if (!valid_desc(desc) || desc->d > 256 || desc->vbits == 0) return false;
+    if (B < 0 || total_q < 0 || max_q < 0 || max_kv_len < 0) return false;
+    if (Hq < 1 || Hq % desc->n_kv_heads || Hq / desc->n_kv_heads > 8) return false;
+    return int64_t(total_q) * Hq <= INT32_MAX && int64_t(B) * desc->n_kv_heads <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" size_t tq_cross_workspace_bytes(const tq_cache_desc *desc, int B, int total_q, int max_q, int Hq,
+                                           int max_kv_len) {
+    if (!cross_sizes_ok(desc, B, total_q, max_q, Hq, max_kv_len)) return 0;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    return tq::cross_ws_bytes(L, cross_shape(B, total_q, max_q, Hq, max_kv_len));
+}
+
+extern "C" int tq_cross_attn(const tq_params *kp, const tq_params *vp, const tq_cache_desc *desc, const void *Q,
+                             int total_q, int max_q, int Hq, const int32_t *cu_q, int B, const int32_t *block_table,
+                             int max_blocks, const int32_t *kv_lens, int max_kv_len, const void *cache,
+                             int64_t num_blocks, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+    if (!attn_params_ok(kp, vp, desc, Hq)) {
+        if (valid_desc(desc) && (desc->d > 256 || (Hq >= 1 && Hq % desc->n_kv_heads == 0 &&
+                                                   Hq / desc->n_kv_heads > 8)))
+            return TQ_EUNSUPPORTED;
+        return TQ_EINVAL;
+    }
+    if (!cross_sizes_ok(desc, B, total_q, max_q, Hq, max_kv_len) || max_blocks < 0 || num_blocks < 0)
+        return TQ_EINVAL;
+    if (B == 0 || total_q == 0 || max_q == 0) return TQ_OK;
+    if (!Q || !cu_q || !block_table || !kv_lens || !cache || !out || !workspace) return TQ_EINVAL;
+    if (!aligned(Q, 16) || !aligned(cache, 256) || !aligned(workspace, 256) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4))
+        return TQ_EINVAL;
+    if (int64_t(max_blocks) * desc->page_tokens < max_kv_len) return TQ_EINVAL;
+    int device = -1;
+    if (cudaGetDevice(&device) != cudaSuccess) return TQ_ECUDA;
+    if (kp->device != device || vp->device != device) return TQ_EINVAL;
+    tq::Layout L;
+    tq::make_layout(*desc, &L);
+    tq::CrossShape s = cross_shape(B, total_q, max_q, Hq, max_kv_len);
+    s.cu_q = cu_q;
+    s.block_table = block_table;
+    s.kv_lens = kv_lens;
+    s.max_blocks = max_blocks;
+    if (workspace_bytes < tq::cross_ws_bytes(L, s)) return TQ_EINVAL;
+    return cuda_status(tq::launch_cross(kp, vp, L, Q, s, static_cast<const uint8_t *>(cache), num_blocks, out, lse,
+                                        static_cast<uint8_t *>(workspace), stream));
+}
+
 extern "C" size_t tq_pages_workspace_bytes(int64_t num_blocks, int n_rows, int max_blocks) {
     if (num_blocks < 1 || num_blocks > INT32_MAX || n_rows < 1 || max_blocks < 1) return 0;
     return tq::pages_ws_bytes(num_blocks, n_rows, max_blocks);

@@ -466,6 +466,11 @@ struct CombineArgs {
     DevParams vp;
     void *out;          // bf16 [n_seq][Hq][D]
     float *lse;         // optional [n_seq][Hq]
+    // cross attention: rows with a negative length are not written, and a
+    // query with a coordinate that is not finite gives NaN (the online softmax
+    // drops NaN logits from its maximum and would leave zeros)
+    const int32_t *row_lens;   // optional [n_seq]
+    const __nv_bfloat16 *Q;    // with row_lens: [n_seq][Hq][D]
 };
 
 // One warp per (group, head): merge splits by log-sum-exp, rotate back.  The
@@ -479,6 +484,7 @@ __global__ void __launch_bounds__(128) combine_kernel(CombineArgs a) {
     const int64_t r = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (r >= int64_t(a.n_groups) * a.G) return;
     const int g = int(r / a.G), h = int(r - int64_t(g) * a.G);
+    if (a.row_lens && a.row_lens[g / a.H] < 0) return;
     auto pb = [&](int s) { return (int64_t(g) * a.n_splits + s) * a.G + h; };
     float M = -INFINITY;
     for (int s = lane; s < a.n_splits; s += 32) M = fmaxf(M, a.part_ml[pb(s) * 2]);
@@ -526,11 +532,18 @@ __global__ void __launch_bounds__(128) combine_kernel(CombineArgs a) {
         }
     }
     Lsum = warp_sum(Lsum);
-    const float inv = Lsum > 0.f ? 1.0f / Lsum : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= inv;
+    float inv = Lsum > 0.f ? 1.0f / Lsum : 0.f;
     const int b = g / a.H, kvh = g - b * a.H;
     const int64_t orow = int64_t(b) * a.Hq + int64_t(kvh) * a.G + h;
+    if (a.row_lens && a.row_lens[b] > 0) {
+        float q[E], worst = 0.f;
+        load_vec<D>(a.Q + orow * D, lane, q);
+#pragma unroll
+        for (int e = 0; e < E; ++e) worst += q[e] * 0.f;   // 0, or NaN
+        inv += warp_sum(worst);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= inv;
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D;
     if (a.vp.rot) {
         // o = R^T o_r with the dense rotation: rows of its transpose
@@ -555,7 +568,7 @@ __global__ void __launch_bounds__(128) combine_kernel(CombineArgs a) {
             for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(o[e] * rs * sg[e]);
         }
     }
-    if (a.lse && lane == 0) a.lse[orow] = Lsum > 0.f ? M + logf(Lsum) : -INFINITY;
+    if (a.lse && lane == 0) a.lse[orow] = inv != inv ? inv : Lsum > 0.f ? M + logf(Lsum) : -INFINITY;
 }
 
 struct Plan {
@@ -703,6 +716,8 @@ int run_attention(const tq_params *kp, const tq_params *vp, const Layout &L, con
     c.vp = vp->dev;
     c.out = out;
     c.lse = lse;
+    c.row_lens = s.skip_negative ? s.seq_lens : nullptr;
+    c.Q = static_cast<const __nv_bfloat16 *>(Q);
     const int64_t crow = int64_t(p.n_groups) * p.G;
     combine_kernel<D><<<unsigned((crow + 3) / 4), 128, 0, st>>>(c);
     return cudaGetLastError();

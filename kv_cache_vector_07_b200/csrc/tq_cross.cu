@@ -1,0 +1,96 @@
+// Cross attention: runs of queries, each seeing the whole cache of its
+// sequence (an encoder's states, of another length than the run).
+//
+//   l_t = (nhat_t <Rq, c[code_t]> + rho_t sqrt(pi/2)/m <S R q, 2 s_t - 1>) / sqrt(d)
+//   o   = R_v^T sum_t softmax(l)_t nhat_v,t c_v[code_v,t]
+//
+// By rows: every query row becomes a decode row of its own, with its
+// sequence's table row and length, and the decode kernels read the compressed
+// pages once for each.  Right for every codec and head size; what it reads
+// grows with the run.
+#include <cuda_runtime.h>
+
+#include "tq_dev.cuh"
+
+namespace tq {
+namespace {
+
+struct RowsArgs {
+    const int32_t *cu_q, *table, *kv_lens;
+    int B, total_q, max_q, bt_stride, max_kv_len, P, width;
+    int32_t *row_len;        // [total_q], -1: the row belongs to no run
+    int32_t *row_table;      // [total_q][width]
+    uint32_t *status;
+};
+
+// One warp per query row: its sequence (the last b with cu_q[b] <= row), that
+// sequence's length and its table row.
+__global__ void __launch_bounds__(128) cross_rows_kernel(RowsArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int row = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= a.total_q) return;
+    int lo = 0, hi = a.B;                                  // cu_q[lo] <= row (or lo = 0), lo < hi
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_q[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    int len = -1;
+    const int begin = a.cu_q[lo];
+    if (row >= begin && row < a.cu_q[lo + 1]) {
+        if (row - begin < a.max_q) len = min(max(a.kv_lens[lo], 0), a.max_kv_len);
+        else if (lane == 0) atomicOr(a.status, TQ_DEV_ROW);
+    }
+    if (lane == 0) a.row_len[row] = len;
+    const int pages = len > 0 ? (len + a.P - 1) / a.P : 0;
+    for (int j = lane; j < pages; j += 32)
+        a.row_table[int64_t(row) * a.width + j] = a.table[int64_t(lo) * a.bt_stride + j];
+}
+
+AttnShape rows_shape(const Layout &L, const CrossShape &s) {
+    AttnShape r{};
+    r.n_seq = s.total_q;
+    r.Hq = s.Hq;
+    r.max_blocks = (s.max_kv_len + L.P - 1) / L.P;
+    r.bt_stride = r.max_blocks;
+    r.is_decode = 1;
+    r.skip_negative = 1;
+    r.max_len = s.max_kv_len;
+    return r;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t cross_ws_bytes(const Layout &L, const CrossShape &s) {
+    const AttnShape r = rows_shape(L, s);
+    return up256(attn_ws_bytes(L, r)) + up256(4 * size_t(s.total_q)) +
+           up256(4 * size_t(s.total_q) * size_t(r.max_blocks));
+}
+
+int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
+                 const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream) {
+    AttnShape r = rows_shape(L, s);
+    const size_t inner = up256(attn_ws_bytes(L, r));
+    RowsArgs a;
+    a.cu_q = s.cu_q;
+    a.table = s.block_table;
+    a.kv_lens = s.kv_lens;
+    a.B = s.B;
+    a.total_q = s.total_q;
+    a.max_q = s.max_q;
+    a.bt_stride = s.max_blocks;
+    a.max_kv_len = s.max_kv_len;
+    a.P = L.P;
+    a.width = r.max_blocks;
+    a.row_len = reinterpret_cast<int32_t *>(ws + inner);
+    a.row_table = reinterpret_cast<int32_t *>(ws + inner + up256(4 * size_t(s.total_q)));
+    a.status = reinterpret_cast<uint32_t *>(ws);
+    cross_rows_kernel<<<unsigned((s.total_q + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    r.seq_lens = a.row_len;
+    r.block_table = a.row_table;
+    return launch_attention(kp, vp, L, Q, r, cache, num_blocks, out, lse, nullptr, 0, ws, inner, stream);
+}
+
+}  // namespace tq

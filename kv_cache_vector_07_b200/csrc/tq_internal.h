@@ -185,6 +185,7 @@ struct AttnShape {
     int base_len;         // prefill: seq_len - C (query j sees base_len + j + 1)
     int max_len;          // longest visible length
     int is_decode;        // 1: decode (per-sequence lengths), 0: prefill chunk
+    int skip_negative;    // 1: rows of a sequence with a negative length are not written
 };
 // New tokens of a fused decode step (one per sequence): bf16 K and V
 // [B][H][d], their slots, and the cache they are written into.
@@ -229,6 +230,17 @@ int launch_pf128(const tq_params *kp, const tq_params *vp, const Layout &L, cons
 // Head norms with rotary positions (arguments checked by the caller).
 int launch_rope(const tq_rope_desc &rd, int dtype, int w_dtype, int64_t n, const tq_heads *q, const tq_heads *k,
                 const int32_t *positions, int64_t axis_stride, const float *inv_freq, void *stream);
+
+// Cross attention (arguments checked by the caller): runs of queries over
+// each sequence's whole cache.
+struct CrossShape {
+    int B, total_q, max_q, Hq;
+    const int32_t *cu_q, *block_table, *kv_lens;
+    int max_blocks, max_kv_len;
+};
+size_t cross_ws_bytes(const Layout &L, const CrossShape &s);
+int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
+                 const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream);
 
 // Pages of a cache (arguments checked by the caller).
 size_t pages_ws_bytes(int64_t num_blocks, int n_rows, int max_blocks);

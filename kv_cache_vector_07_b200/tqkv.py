@@ -118,6 +118,9 @@ _sig("tq_prefill_attn", _i32, [_vp, _vp, ctypes.POINTER(CacheDesc), _vp, _i32, _
 _sig("tq_score_workspace_bytes", _sz, [ctypes.POINTER(CacheDesc), _i64, _i32, _i32])
 _sig("tq_score", _i32, [_vp, ctypes.POINTER(CacheDesc), _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
 _pool_p, _desc_p, _ptrs = ctypes.POINTER(_PagePool), ctypes.POINTER(CacheDesc), ctypes.POINTER(_vp)
+_sig("tq_cross_workspace_bytes", _sz, [_desc_p, _i32, _i32, _i32, _i32, _i32])
+_sig("tq_cross_attn", _i32, [_vp, _vp, _desc_p, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _vp,
+                             _vp, _vp, _sz, _vp])
 _sig("tq_pages_workspace_bytes", _sz, [_i64, _i32, _i32])
 _sig("tq_pages_reserve", _i32, [_desc_p, _pool_p, _vp, _vp, _i64, _vp, _sz, _vp])
 _sig("tq_pages_fork", _i32, [_desc_p, _pool_p, _ptrs, _i32, _vp, _vp, _i32, _vp, _sz, _vp])
@@ -428,6 +431,49 @@ def score(p: Params, desc: CacheDesc, db_cache: torch.Tensor, n_db: int, Q: torc
     _check(_lib.tq_score(p.handle, ctypes.byref(desc), _ptr(db_cache), n_db, _ptr(Q), n_q, k, _ptr(top_scores),
                          _ptr(top_idx), _ptr(workspace), workspace.numel(), _stream(stream)), "tq_score")
     return top_scores, top_idx
+
+
+# ---------------------------------------------------------------------------
+# cross attention
+# ---------------------------------------------------------------------------
+def cross_workspace_bytes(desc: CacheDesc, B: int, total_q: int, max_q: int, Hq: int, max_kv_len: int) -> int:
+    return int(_lib.tq_cross_workspace_bytes(ctypes.byref(desc), B, total_q, max_q, Hq, max_kv_len))
+
+
+def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: torch.Tensor, max_q: int,
+               block_table: torch.Tensor, kv_lens: torch.Tensor, max_kv_len: int, cache: torch.Tensor,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """tq_cross_attn: the queries cu_q[b] .. cu_q[b + 1] - 1 of Q bf16 [total_q,
+    Hq, d] see all kv_lens[b] tokens of sequence b (block_table [B, max_blocks]).
+    Rows of out that belong to no run are not written (zero where out is not
+    given).  lse fp32 [total_q, Hq], optional."""
+    _dev_check(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
+    dev = _same_device(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
+    if Q.dim() != 3 or Q.shape[2] != desc.d or Q.dtype != torch.bfloat16:
+        raise ValueError("Q must be bf16 [total_q, Hq, d]")
+    B = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or kv_lens.shape != (B,) or cu_q.shape != (B + 1,):
+        raise ValueError("block_table must be [B, max_blocks], kv_lens [B] and cu_q [B + 1]")
+    if any(t.dtype != torch.int32 for t in (cu_q, block_table, kv_lens)):
+        raise ValueError("cu_q, block_table and kv_lens must be int32")
+    if cache.dtype != torch.uint8 or cache.shape[1:] != (desc.n_kv_heads, cache_bytes(desc)):
+        raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
+    if out is not None and (out.shape != Q.shape or out.dtype != Q.dtype):
+        raise ValueError("out must have Q's shape and dtype")
+    total_q, Hq, _ = Q.shape
+    if lse is not None and (lse.shape != (total_q, Hq) or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [total_q, Hq]")
+    with _on(dev):
+        if out is None:
+            out = torch.zeros_like(Q)
+        if workspace is None:
+            workspace = _workspace(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), Q.device)
+        _check(_lib.tq_cross_attn(kp.handle, vp.handle, ctypes.byref(desc), _ptr(Q), total_q, max_q, Hq, _ptr(cu_q), B,
+                                  _ptr(block_table), block_table.shape[1], _ptr(kv_lens), max_kv_len, _ptr(cache),
+                                  cache.shape[0], _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "tq_cross_attn")
+    return out
 
 
 # ---------------------------------------------------------------------------
