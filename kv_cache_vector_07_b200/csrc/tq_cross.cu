@@ -63,14 +63,20 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+// The size does not know the rotation of the parameters: it covers both ways.
 size_t cross_ws_bytes(const Layout &L, const CrossShape &s) {
     const AttnShape r = rows_shape(L, s);
-    return up256(attn_ws_bytes(L, r)) + up256(4 * size_t(s.total_q)) +
-           up256(4 * size_t(s.total_q) * size_t(r.max_blocks));
+    const size_t rows = up256(attn_ws_bytes(L, r)) + up256(4 * size_t(s.total_q)) +
+                        up256(4 * size_t(s.total_q) * size_t(r.max_blocks));
+    if (!cross_tc_covers(L, false, s)) return rows;
+    const size_t tc = cross_tc_ws_bytes(L, s);
+    return tc > rows ? tc : rows;
 }
 
 int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
                  const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream) {
+    if (cross_tc_covers(L, kp->dev.rot || vp->dev.rot, s))
+        return launch_cross_tc(kp, vp, L, Q, s, cache, num_blocks, out, lse, ws, static_cast<cudaStream_t>(stream));
     AttnShape r = rows_shape(L, s);
     const size_t inner = up256(attn_ws_bytes(L, r));
     RowsArgs a;

@@ -1,0 +1,885 @@
+// Cross attention on the tensor cores, for head sizes 64 and 128 under the
+// Hadamard rotation, any codec, any page size.
+//
+//   k_t = nhat_t c[code_t] + rho_t sqrt(pi/2)/m S^T (2 s_t - 1),  v_t = nhat_v,t c_v[code_v,t]
+//   o   = R_v^T sum_t softmax_t(<R q, k_t> / sqrt(d)) v_t
+//
+// Every query of a run reads the same states, so they are decoded once:
+//
+//   expand   128 tokens of one KV head at a time: k_t and v_t in their rotated
+//            bases as fp16 operand tiles in the workspace, laid out as the
+//            tensor cores read them from shared memory.  S^T s is a product of
+//            +-1 signs (exact) with S as fp16 (exact for |S| >= 2^-14) on
+//            tcgen05.  A tile is scaled by a power of two to a largest
+//            magnitude in [2^10, 2^11), so keys of any norm keep fp16's 11
+//            bits down to 2^-25 of the tile's largest coordinate.
+//   attend   256 query rows (two tiles of 128 rows: positions x heads of the
+//            group) walk the tiles: S = Q K^T and O += P V on tcgen05, the
+//            online softmax between them, a thread per row.
+//
+// Queries are rotated and scaled to fp16 as they are staged (the same range),
+// softmax weights are fp16, all sums fp32: each operand is off by at most
+// 2^-11 of itself, eight times finer than the bf16 result.  The tile scales
+// ride along for nothing: the key's on the factor that turns S into a
+// logarithm, the value's (2^e) on its offset, P' = 2^(l + e - m) with m the
+// running maximum of l + e, while the sum takes P' 2^-e.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "tc05.cuh"
+#include "tq_dev.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kTile = 128;                 // keys of a tile, and query rows of one
+
+// What the attention needs of a tile beside its operands.
+struct __align__(32) TileMeta {
+    float kscale;                          // key = stored * kscale
+    float vexp, vinv;                      // value = stored * 2^vexp; vinv = 2^-vexp
+    float unused;
+    uint32_t mask[4];                      // key k of the tile is there
+};
+
+constexpr size_t image_bytes(int d) { return size_t(kTile) * d * 2; }   // one operand tile
+
+__device__ __forceinline__ uint32_t h2u(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(tc05::smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Bounded wait: about a second.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < 500000u; ++i)
+        if (tc05::mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+    return false;
+}
+
+// Bounded wait (about a second) that also gives up once another thread has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag) {
+    for (uint32_t i = 0; i < 500000u; ++i) {
+        if (tc05::mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+        if ((i & 63u) == 63u && *abort_flag) return false;
+    }
+    *abort_flag = 1u;
+    return false;
+}
+
+// ---------------------------------------------------------------------------
+// expand
+// ---------------------------------------------------------------------------
+struct ExpandArgs {
+    Layout L;
+    DevParams kp, vp;
+    const int32_t *table, *kv_lens;
+    int bt_stride, max_kv_len;
+    const uint8_t *cache;
+    int64_t num_blocks;
+    int pair0, n_pairs, n_tiles;           // pairs (sequence, KV head) of this launch
+    uint8_t *images;                       // [pair][tile][keys | values]
+    TileMeta *meta;                        // [pair][tile]
+    uint32_t *status;
+};
+
+struct CodeTables {
+    float lv[16], lv2[8], polar[132];
+};
+
+// Eight coordinates (8 cc ..) of a token's reconstruction without its norm.
+template <int D>
+__device__ __forceinline__ void levels8(const CodeTables &tab, const uint8_t *page, int pos, int cc, bool polar,
+                                        bool fp8, bool half, int a_bits, int b_bits, int off, int bpt, int w, int hoff,
+                                        int hbpt, int off2, int bpt2, int w2, int hoff2, int hbpt2, float (&y)[8]) {
+    if (polar) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float2 v = polar_pair<D>(page + off + pos * bpt, page + off2 + pos * bpt2, tab.polar, 4 * cc + p);
+            y[2 * p] = v.x;
+            y[2 * p + 1] = v.y;
+        }
+        return;
+    }
+    const bool second = half && cc >= D / 16;
+    const int c = second ? cc - D / 16 : cc;
+    const int width = second ? w2 : w;
+    const uint8_t *at = page + (second ? off2 + pos * bpt2 : off + pos * bpt) + c * width;
+    if (fp8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+        const float s = rsqrtf(float(D));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = s * e4m3_to_float(uint8_t((e < 4 ? v.x : v.y) >> (8 * (e & 3))));
+        return;
+    }
+    uint32_t bits;
+    if (width == 4) bits = *reinterpret_cast<const uint32_t *>(at);
+    else if (width == 2) bits = *reinterpret_cast<const uint16_t *>(at);
+    else bits = *at;
+    uint32_t high = 0;
+    if ((second ? b_bits : a_bits) == 3) high = page[(second ? hoff2 + pos * hbpt2 : hoff + pos * hbpt) + c];
+    const float *lv = second ? tab.lv2 : tab.lv;
+    const uint32_t m = (1u << width) - 1u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = lv[((bits >> (e * width)) & m) | (((high >> e) & 1u) << 2)];
+}
+
+template <int D>
+constexpr size_t expand_smem() { return size_t(D) * D * 2 + 2 * image_bytes(D) + 1024; }
+
+// Power-of-two scale of a tile from its largest magnitude; *e: value = stored * 2^e.
+__device__ __forceinline__ float tile_scale(float mx, int *e) {
+    int ex = 11;
+    if (mx > 0.f && mx < INFINITY) frexpf(mx, &ex);
+    *e = ex - 11;
+    return ldexpf(1.f, 11 - ex);
+}
+
+// Persistent over (pair, tile); 256 threads, thread (key, half of its
+// coordinates).
+template <int D>
+__global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_constant__ ExpandArgs a) {
+    constexpr int HALF = D / 2, NC = D / 16;          // coordinates and 16-byte chunks of a thread
+    constexpr uint32_t kImg = uint32_t(image_bytes(D));
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t tmem_holder;
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ float red[2][8];
+    __shared__ CodeTables tk, tv;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sS = sm, *sK = sm + D * D * 2, *sV = sK + kImg;
+    const Layout &L = a.L;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int key = tid & 127, hh = tid >> 7;
+
+    // S as the B operand: row j holds S[j][0 .. D), 64 columns to a half
+    if (L.kqjl)
+        for (int i = tid; i < D * D / 8; i += 256) {
+            const int j = i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4 *>(sS + (c >> 3) * (D * 128) + tc05::sw128_offset(uint32_t(j), uint32_t(c & 7))) =
+                *reinterpret_cast<const uint4 *>(a.kp.S16 + size_t(j) * D + c * 8);
+        }
+    if (tid < 16) {
+        tk.lv[tid] = (L.ka_bits <= 4 && tid < (1 << L.ka_bits)) ? a.kp.lv[tid] : 0.f;
+        tv.lv[tid] = (L.va_bits <= 4 && tid < (1 << L.va_bits)) ? a.vp.lv[tid] : 0.f;
+        if (tid < 8) {
+            tk.lv2[tid] = (L.khalf && tid < (1 << L.kb_bits)) ? a.kp.lv2[tid] : 0.f;
+            tv.lv2[tid] = (L.vhalf && tid < (1 << L.vb_bits)) ? a.vp.lv2[tid] : 0.f;
+        }
+    }
+    for (int i = tid; i < 132; i += 256) {
+        tk.polar[i] = L.kpolar ? a.kp.polar[i] : 0.f;
+        tv.polar[i] = L.vpolar ? a.vp.polar[i] : 0.f;
+    }
+    if (warp == 0) {
+        tc05::tmem_alloc(&tmem_holder, D);
+        tc05::tmem_relinquish();
+        if (lane == 0) {
+            tc05::mbar_init(&bar, 1);
+            tc05::fence_mbar_init();
+        }
+    }
+    tc05::fence_proxy_async_smem();
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = tmem_holder, lrow = uint32_t((warp & 3) * 32) << 16;
+    const float cq = 1.2533141373155003f / float(D);   // sqrt(pi/2) / m
+    uint32_t phase = 0;
+    bool timeout = false;
+
+    const int64_t items = int64_t(a.n_pairs) * a.n_tiles;
+    for (int64_t item = blockIdx.x; item < items && !timeout; item += gridDim.x) {
+        const int pl = int(item / a.n_tiles), tile = int(item - int64_t(pl) * a.n_tiles);
+        const int pair = a.pair0 + pl, b = pair / L.H, h = pair - b * L.H;
+        const int len = min(max(a.kv_lens[b], 0), a.max_kv_len);
+        if (tile * kTile >= len) continue;
+        if (tid == 0) bulk_wait_read();                // the tiles of the item before have been read
+        __syncthreads();
+        const int t = tile * kTile + key, pos = t % L.P;
+        const uint8_t *page = nullptr;
+        if (t < len) {
+            const int blk = a.table[int64_t(b) * a.bt_stride + t / L.P];
+            if (blk >= 0 && blk < a.num_blocks) page = a.cache + (int64_t(blk) * L.H + h) * int64_t(L.page_bytes);
+            else atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
+        }
+        if (L.kqjl) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int cc = hh * NC + c;
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (page) {
+                    const uint32_t bits = page[L.ks_off + pos * L.ks_bpt + cc];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {      // +1 where the bit is set, else -1
+                        const uint32_t u = bits >> (2 * q);
+                        w[q] = 0xBC00BC00u ^ (((u << 15) & 0x8000u) | ((u << 30) & 0x80000000u));
+                    }
+                }
+                *reinterpret_cast<uint4 *>(sK + (cc >> 3) * 16384 + tc05::sw128_offset(uint32_t(key), uint32_t(cc & 7))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            tc05::fence_proxy_async_smem();
+            tc05::fence_before_sync();
+            __syncthreads();
+            if (tid == 0) {
+                tc05::fence_after_sync();
+                constexpr uint32_t idesc = tc05::idesc_f16_f32(128, D) | tc05::kIdescBMajorMN;
+                const uint32_t A = tc05::smem_u32(sK), B = tc05::smem_u32(sS);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc05::mma_f16(tmem, tc05::desc_kmajor_sw128(A + uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u),
+                                  tc05::desc_mnmajor_sw128(B + uint32_t(ks) * 2048u, uint32_t(D) * 128u, 1024u), idesc,
+                                  ks > 0);
+                tc05::mma_commit(&bar);
+            }
+        }
+        // values, while the product runs
+        float y[HALF], mx = 0.f;
+        const float nv = page ? h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.vn_off + pos * 2)) : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (page)
+                levels8<D>(tv, page, pos, hh * NC + c, L.vpolar, false, L.vhalf, L.va_bits, L.vb_bits, L.vc_off, L.vc_bpt,
+                           L.vc_w, L.vh_off, L.vh_bpt, L.vc2_off, L.vc2_bpt, L.vc2_w, L.vh2_off, L.vh2_bpt, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[c * 8 + e] = nv * v[e];
+                mx = fmaxf(mx, fabsf(y[c * 8 + e]));
+            }
+        }
+        mx = warp_max(mx);
+        if (lane == 0) red[0][warp] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[0][i]);
+        int ev;
+        float sc = tile_scale(mx, &ev);
+        auto store = [&](uint8_t *img) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int cc = hh * NC + c;
+                *reinterpret_cast<uint4 *>(img + (cc >> 3) * 16384 + tc05::sw128_offset(uint32_t(key), uint32_t(cc & 7))) =
+                    make_uint4(h2u(y[c * 8] * sc, y[c * 8 + 1] * sc), h2u(y[c * 8 + 2] * sc, y[c * 8 + 3] * sc),
+                               h2u(y[c * 8 + 4] * sc, y[c * 8 + 5] * sc), h2u(y[c * 8 + 6] * sc, y[c * 8 + 7] * sc));
+            }
+        };
+        store(sV);
+        // keys
+        const float nk = page ? h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kn_off + pos * 2)) : 0.f;
+        const float rk = page && L.kqjl ? cq * h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kr_off + pos * 2)) : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (page)
+                levels8<D>(tk, page, pos, hh * NC + c, L.kpolar, L.kbits == 8, L.khalf, L.ka_bits, L.kb_bits, L.kc_off,
+                           L.kc_bpt, L.kc_w, L.kh_off, L.kh_bpt, L.kc2_off, L.kc2_bpt, L.kc2_w, L.kh2_off, L.kh2_bpt, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[c * 8 + e] = nk * v[e];
+        }
+        if (L.kqjl) {
+            const bool ok = __all_sync(kFull, wait_bounded(&bar, phase & 1u));
+            timeout = !ok;
+            ++phase;
+            tc05::fence_after_sync();
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < HALF / 32; ++c) {
+                    uint32_t r[32];
+                    tc05::tmem_ld_32x32b_x32(tmem + lrow + uint32_t(hh * HALF + c * 32), r);
+                    tc05::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[c * 32 + e] = fmaf(rk, __uint_as_float(r[e]), y[c * 32 + e]);
+                }
+            }
+        }
+        mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < HALF; ++e) mx = fmaxf(mx, fabsf(y[e]));
+        mx = warp_max(mx);
+        if (lane == 0) red[1][warp] = mx;
+        const bool out_of_time = __syncthreads_or(timeout);   // also: every thread has its part of the product
+        if (out_of_time) {
+            timeout = true;
+            break;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[1][i]);
+        int ek;
+        sc = tile_scale(mx, &ek);
+        store(sK);
+        const uint32_t there = __ballot_sync(kFull, page != nullptr);
+        TileMeta *m = a.meta + item;
+        if (hh == 0 && lane == 0) m->mask[warp] = there;
+        if (tid == 0) {
+            m->kscale = ldexpf(1.f, ek);
+            m->vexp = float(ev);
+            m->vinv = ldexpf(1.f, -ev);
+            m->unused = 0.f;
+        }
+        tc05::fence_proxy_async_smem();
+        tc05::fence_before_sync();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_s2g(a.images + size_t(item) * 2 * kImg, sK, 2 * kImg);   // keys, then values
+            bulk_commit();
+        }
+    }
+    if (tid == 0) {
+        bulk_wait();
+        if (timeout) atomicOr(a.status, TQ_DEV_WAIT_TIMEOUT);
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc05::fence_after_sync();
+        tc05::tmem_dealloc(tmem, D);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// attend
+// ---------------------------------------------------------------------------
+struct AttendArgs {
+    const __nv_bfloat16 *Q;
+    int Hq, H, G, PT;                      // PT = 128 / G positions of a query tile
+    const int32_t *cu_q, *kv_lens;
+    int total_q, max_q, max_kv_len;
+    int pair0, n_tiles;
+    const uint8_t *images;
+    const TileMeta *meta;
+    const float *ksigns, *vsigns;
+    int n_splits, split_tiles;
+    __nv_bfloat16 *out;
+    float *lse;
+    float *part_o, *part_ml;               // [split][total_q Hq][D], [..][2]
+    uint32_t *status;
+};
+
+// The run of sequence b: its first query, and how many are served.
+__device__ __forceinline__ int run_of(const AttendArgs &a, int b, int *first, bool *cut) {
+    const int q0 = a.cu_q[b], q1 = min(a.cu_q[b + 1], a.total_q);
+    *first = q0;
+    *cut = q0 >= 0 && q1 - q0 > a.max_q;
+    return q0 >= 0 && q1 > q0 ? min(q1 - q0, a.max_q) : 0;
+}
+
+// Unnormalised Walsh-Hadamard transform of a vector in registers.
+template <int D>
+__device__ __forceinline__ void fwht_regs(float (&x)[D]) {
+#pragma unroll
+    for (int s = 1; s < D; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+            if ((i & s) == 0) {
+                const float u = x[i], v = x[i + s];
+                x[i] = u + v;
+                x[i + s] = u - v;
+            }
+}
+
+template <int D>
+constexpr int ring_slots() { return D == 128 ? 5 : 8; }
+constexpr int kMetaSlots = 8;
+constexpr uint32_t kBarBytes = 512;
+template <int D>
+constexpr size_t attend_smem() {
+    return (2 + ring_slots<D>()) * image_bytes(D) + kMetaSlots * sizeof(TileMeta) + kBarBytes + 1024;
+}
+constexpr int kAttendThreads = 320;        // two tiles of softmax rows, the MMA issuer's warp, the loader's
+
+template <int D>
+__global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr uint32_t kImg = uint32_t(image_bytes(D));
+    constexpr int NS = ring_slots<D>();
+    constexpr uint32_t TO = 256;                          // TMEM columns: S / P of the tiles at 0 and 128, O behind
+    const int pl = blockIdx.y, pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H, split = blockIdx.z;
+    int q0;
+    bool cut;
+    const int nq = run_of(a, b, &q0, &cut);
+    if (cut && blockIdx.x == 0 && h == 0 && split == 0 && threadIdx.x == 0) atomicOr(a.status, TQ_DEV_ROW);
+    const int pos0 = int(blockIdx.x) * 2 * a.PT;
+    if (pos0 >= nq) return;
+    const int n_t = pos0 + a.PT < nq ? 2 : 1;
+    const int len = min(max(a.kv_lens[b], 0), a.max_kv_len);
+    const int tile0 = split * a.split_tiles;
+    const int n = min((len + kTile - 1) / kTile - tile0, a.split_tiles);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tt = (tid >> 7) & 1, r = tid & 127;         // softmax threads: query tile and row
+    const int qpos = pos0 + tt * a.PT + r / a.G;
+    const bool row_ok = tid < 256 && r < a.PT * a.G && qpos < nq;
+    const int64_t row = (int64_t(q0) + qpos) * a.Hq + h * a.G + r % a.G;
+    const int64_t prow = int64_t(split) * a.total_q * a.Hq + row;
+
+    if (n <= 0) {                                         // no key of this split
+        if (!row_ok) return;
+        if (a.n_splits > 1) {
+            a.part_ml[prow * 2] = -INFINITY;
+            a.part_ml[prow * 2 + 1] = 0.f;
+        } else {
+            for (int i = 0; i < D / 8; ++i)
+                reinterpret_cast<uint4 *>(a.out + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse) a.lse[row] = -INFINITY;
+        }
+        return;
+    }
+
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t tmem_holder;
+    __shared__ uint32_t abort_word;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = sm, *ring = sm + 2 * kImg;
+    TileMeta *smeta = reinterpret_cast<TileMeta *>(ring + NS * kImg);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + kMetaSlots);
+    uint64_t *kv_full = bars;                             // [NS] operand tile landed
+    uint64_t *kv_empty = bars + 8;                        // [NS] its products done (commit)
+    uint64_t *meta_full = bars + 16;                      // [8]
+    uint64_t *s_full = bars + 24;                         // [2] S of a query tile done (commit)
+    uint64_t *p_full = bars + 26;                         // [2] P written, O rescaled (128)
+    uint64_t *o_done = bars + 28;                         // [2] last product of a tile done (commit)
+    uint64_t *q_full = bars + 30;                         // queries staged (128 a tile)
+    uint64_t *drained = bars + 31;                        // products in flight when a wait gave up
+    volatile uint32_t *abort_flag = &abort_word;
+    if (warp == 8) {
+        tc05::tmem_alloc(&tmem_holder, 512);
+        tc05::tmem_relinquish();
+    }
+    if (tid == 288) {
+        for (int i = 0; i < NS; ++i) {
+            tc05::mbar_init(&kv_full[i], 1);
+            tc05::mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < kMetaSlots; ++i) tc05::mbar_init(&meta_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            tc05::mbar_init(&s_full[i], 1);
+            tc05::mbar_init(&p_full[i], 128);
+            tc05::mbar_init(&o_done[i], 1);
+        }
+        tc05::mbar_init(q_full, uint32_t(128 * n_t));
+        tc05::mbar_init(drained, 1);
+        abort_word = 0u;
+        tc05::fence_mbar_init();
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = tmem_holder;
+    bool timeout = false;
+
+    if (warp == 9) {
+        // ================= loader: K(0), V(0), K(1), V(1), ... through one ring
+        if (lane == 0) {
+            const int64_t at = int64_t(pl) * a.n_tiles + tile0;
+            const uint8_t *img = a.images + size_t(at) * 2 * kImg;
+            int issued = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int s = i % NS, j = i >> 1;
+                if (i >= NS && !wait_or_abort(&kv_empty[s], uint32_t(i / NS - 1) & 1u, abort_flag)) {
+                    timeout = true;
+                    break;
+                }
+                if ((i & 1) == 0) {
+                    // the slot's last reader was tile j - 8, whose softmax is long done: the
+                    // operand slot just found empty is of a later tile
+                    tc05::mbar_expect_tx(&meta_full[j % kMetaSlots], uint32_t(sizeof(TileMeta)));
+                    tc05::bulk_g2s(&smeta[j % kMetaSlots], a.meta + at + j, uint32_t(sizeof(TileMeta)),
+                                   &meta_full[j % kMetaSlots]);
+                }
+                tc05::mbar_expect_tx(&kv_full[s], kImg);
+                tc05::bulk_g2s(ring + s * kImg, img + size_t(i) * kImg, kImg, &kv_full[s]);
+                issued = i + 1;
+            }
+            // copies in flight land before shared memory is given back
+            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) {
+                const int j = i >> 1;
+                if (!wait_bounded(&kv_full[i % NS], uint32_t(i / NS) & 1u)) timeout = true;
+                if ((i & 1) == 0 && !wait_bounded(&meta_full[j % kMetaSlots], uint32_t(j / kMetaSlots) & 1u))
+                    timeout = true;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ================= MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = tc05::idesc_f16_f32(128, 128);
+            constexpr uint32_t idesc_pv = tc05::idesc_f16_f32(128, D) | tc05::kIdescBMajorMN;
+            const uint32_t q_s = tc05::smem_u32(sQ), ring_s = tc05::smem_u32(ring);
+            auto landed = [&](int i) { return wait_or_abort(&kv_full[i % NS], uint32_t(i / NS) & 1u, abort_flag); };
+            auto qk = [&](int t, int i) {                  // S_t = Q_t K^T, K in ring entry i
+                const uint32_t A = q_s + uint32_t(t) * kImg, B = ring_s + uint32_t(i % NS) * kImg;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u;
+                    tc05::mma_f16(tmem + uint32_t(t) * 128u, tc05::desc_kmajor_sw128(A + o), tc05::desc_kmajor_sw128(B + o),
+                                  idesc_qk, ks > 0);
+                }
+                tc05::mma_commit(&s_full[t]);
+            };
+            auto pv = [&](int t, int i, bool add) {        // O_t += P_t V, V in ring entry i
+                const uint32_t B = ring_s + uint32_t(i % NS) * kImg;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc05::mma_f16_ts(tmem + TO + uint32_t(t * D), tmem + uint32_t(t) * 128u + uint32_t(ks) * 8u,
+                                     tc05::desc_mnmajor_sw128(B + uint32_t(ks) * 2048u, 16384u, 1024u), idesc_pv,
+                                     add || ks > 0);
+            };
+            int started = 0;                               // s_full commits per tile so far (all tiles alike)
+            bool ok = wait_or_abort(q_full, 0u, abort_flag) && landed(0);
+            if (ok) {
+                tc05::fence_after_sync();
+                for (int t = 0; t < n_t; ++t) qk(t, 0);
+                tc05::mma_commit(&kv_empty[0]);
+                started = 1;
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
+                for (int t = 0; t < n_t && ok; ++t) {
+                    ok = wait_or_abort(&p_full[t], uint32_t(j) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                    pv(t, 2 * j + 1, j > 0);
+                    if (t == n_t - 1) tc05::mma_commit(&kv_empty[(2 * j + 1) % NS]);
+                    if (j + 1 < n) {
+                        // in issue order behind the product that reads P from the same columns
+                        qk(t, 2 * j + 2);
+                        if (t == n_t - 1) tc05::mma_commit(&kv_empty[(2 * j + 2) % NS]);
+                    } else {
+                        tc05::mma_commit(&o_done[t]);
+                    }
+                }
+            }
+            timeout = !ok;
+            if (timeout && started) {
+                // what was issued completes before TMEM and shared memory are given back
+                tc05::mma_commit(drained);
+                wait_bounded(drained, 0u);
+            }
+        }
+        __syncwarp();
+    } else if (tt < n_t) {
+        // ================= softmax: a thread per query row
+        const uint32_t lrow = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lrow + uint32_t(tt) * 128u, to = tmem + lrow + TO + uint32_t(tt * D);
+        float rowc = 1.f;
+        bool finite = true;
+        {
+            float x[D];
+            if (row_ok) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.Q + row * D);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 u = src[c];
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[8 * c + 2 * e] = __uint_as_float(w[e] << 16) * a.ksigns[8 * c + 2 * e];
+                        x[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * a.ksigns[8 * c + 2 * e + 1];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D; ++i) x[i] = 0.f;
+            }
+            fwht_regs<D>(x);
+            float mx = 0.f, bad = 0.f;
+#pragma unroll
+            for (int i = 0; i < D; ++i) {
+                mx = fmaxf(mx, fabsf(x[i]));
+                bad += x[i] * 0.f;
+            }
+            finite = bad == 0.f;                           // a coordinate that is not finite spreads over the row
+            int e;
+            const float down = tile_scale(finite ? mx : 0.f, &e);
+            // log2(e) / sqrt(d) of the logit, 1 / sqrt(d) of the rotation
+            rowc = ldexpf(1.4426950408889634f / float(D), e);
+            uint8_t *dst = sQ + uint32_t(tt) * kImg;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + tc05::sw128_offset(uint32_t(r), uint32_t(c & 7))) =
+                    make_uint4(h2u(x[8 * c] * down, x[8 * c + 1] * down), h2u(x[8 * c + 2] * down, x[8 * c + 3] * down),
+                               h2u(x[8 * c + 4] * down, x[8 * c + 5] * down), h2u(x[8 * c + 6] * down, x[8 * c + 7] * down));
+        }
+        tc05::fence_proxy_async_smem();
+        tc05::mbar_arrive(q_full);
+        // waits decided per warp, so the warp-wide TMEM accesses stay converged
+        auto wait_w = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(kFull, wait_or_abort(bar, parity, abort_flag));
+        };
+        float m = -INFINITY, l = 0.f;                      // log2 units
+        for (int j = 0; j < n; ++j) {
+            if (!wait_w(&meta_full[j % kMetaSlots], uint32_t(j / kMetaSlots) & 1u) ||
+                !wait_w(&s_full[tt], uint32_t(j) & 1u)) {
+                timeout = true;
+                break;
+            }
+            tc05::fence_after_sync();
+            const float4 sc = *reinterpret_cast<const float4 *>(&smeta[j % kMetaSlots]);
+            const uint4 mask = *reinterpret_cast<const uint4 *>(smeta[j % kMetaSlots].mask);
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tc05::tmem_ld_32x32b_x32(ts + uint32_t(c * 32), reinterpret_cast<uint32_t(&)[32]>(s[c * 32]));
+            tc05::tmem_wait_ld();
+            if ((mask.x & mask.y & mask.z & mask.w) != 0xFFFFFFFFu) {
+                const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (!((mw[i >> 5] >> (i & 31)) & 1u)) s[i] = -INFINITY;
+            }
+            float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            const float c2 = fmaxf(rowc * sc.x, 1e-37f);
+            const float top = fmaf(mx, c2, sc.y);
+            // the reference moves only when it is beaten by 2^8: weights stay
+            // within fp16, and O is rescaled a few times a row, not every tile
+            const bool move = top > m + 8.f;
+            const float alpha = move ? exp2f(m - top) : 1.f;
+            if (move) {
+                m = top;
+                l *= alpha;
+            }
+            if (j > 0 && __any_sync(kFull, move)) {
+                // S of this tile was issued behind the last product into O: O is stable
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tc05::tmem_ld_32x32b_x32(to + uint32_t(c * 32), o);
+                    tc05::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tc05::tmem_st_32x32b_x32(to + uint32_t(c * 32), o);
+                }
+            }
+            const float off = m == -INFINITY ? 0.f : sc.y - m;
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p0 = ex2_approx(fmaf(s[c * 32 + 2 * e], c2, off));
+                    const float p1 = ex2_approx(fmaf(s[c * 32 + 2 * e + 1], c2, off));
+                    sum4[(2 * e) & 3] += p0;
+                    sum4[(2 * e + 1) & 3] += p1;
+                    p[e] = h2u(p0, p1);
+                }
+                tc05::tmem_st_32x32b_x16(ts + uint32_t(c * 16), p);
+            }
+            l = fmaf((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]), sc.z, l);
+            tc05::tmem_wait_st();
+            tc05::fence_before_sync();
+            tc05::mbar_arrive(&p_full[tt]);
+        }
+        if (!timeout && !wait_w(&o_done[tt], 0u)) timeout = true;
+        tc05::fence_after_sync();
+        if (!finite) l = __uint_as_float(0x7FC00000u);
+        float o[D];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            tc05::tmem_ld_32x32b_x32(to + uint32_t(c * 32), reinterpret_cast<uint32_t(&)[32]>(o[c * 32]));
+        tc05::tmem_wait_ld();
+        if (row_ok && a.n_splits > 1) {
+            float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D);
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            a.part_ml[prow * 2] = m;
+            a.part_ml[prow * 2 + 1] = l;
+        } else if (row_ok) {
+            fwht_regs<D>(o);
+            const float inv = (l != l || l > 0.f ? 1.f / l : 0.f) * rsqrtf(float(D));
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * c + 2 * e;
+                    const __nv_bfloat162 v =
+                        __floats2bfloat162_rn(o[i] * inv * a.vsigns[i], o[i + 1] * inv * a.vsigns[i + 1]);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (a.lse) a.lse[row] = l != l ? l : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc05::fence_after_sync();
+        tc05::tmem_dealloc(tmem, 512);
+    }
+    if (timeout) atomicOr(a.status, TQ_DEV_WAIT_TIMEOUT);
+}
+
+// Merges the splits of a row: one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int pair = a.pair0 + blockIdx.y, b = pair / a.H, h = pair - b * a.H;
+    const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    int q0;
+    bool cut;
+    const int nq = run_of(a, b, &q0, &cut);
+    if (i >= nq * a.G) return;
+    const int64_t row = (int64_t(q0) + i / a.G) * a.Hq + h * a.G + i % a.G;
+    const int64_t step = int64_t(a.total_q) * a.Hq;
+    float M = -INFINITY;
+    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, a.part_ml[(s * step + row) * 2]);
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int s = 0; s < a.n_splits; ++s) {
+        const float ls = a.part_ml[(s * step + row) * 2 + 1];
+        if (ls == 0.f) continue;                          // no key there
+        const float f = exp2f(a.part_ml[(s * step + row) * 2] - M);
+        l = fmaf(ls, f, l);
+        float v[E];
+        load_vec<D>(a.part_o + (s * step + row) * D, lane, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], f, o[e]);
+    }
+    fwht_warp<D>(o, lane);
+    float sg[E];
+    load_vec<D>(a.vsigns, lane, sg);
+    const float inv = (l != l || l > 0.f ? 1.f / l : 0.f) * rsqrtf(float(D));
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv * sg[e]);
+    if (a.lse && lane == 0) a.lse[row] = l != l ? l : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Sizes of a call: the workspace holds the operand tiles of as many (sequence,
+// KV head) pairs as fit kImageBudget (at least one), round after round.
+constexpr size_t kImageBudget = size_t(1) << 30;
+
+struct TcPlan {
+    int n_tiles, pairs, round, x, n_splits, split_tiles;
+    size_t off_meta, off_img, off_po, off_pml, total;
+};
+
+TcPlan tc_plan(const Layout &L, const CrossShape &s) {
+    TcPlan p{};
+    const int G = s.Hq / L.H, PT = kTile / G;
+    p.n_tiles = (s.max_kv_len + kTile - 1) / kTile;
+    if (p.n_tiles < 1) p.n_tiles = 1;
+    p.pairs = s.B * L.H;
+    const size_t pair_bytes = size_t(p.n_tiles) * 2 * image_bytes(L.d);
+    size_t fit = kImageBudget / pair_bytes;
+    if (fit < 1) fit = 1;
+    if (fit > 65535) fit = 65535;
+    p.round = int(fit < size_t(p.pairs) ? fit : size_t(p.pairs));
+    p.x = (s.max_q + 2 * PT - 1) / (2 * PT);
+    // few blocks: the key axis is split, into pieces of at least four tiles
+    const int64_t blocks = int64_t(p.x) * p.round;
+    int sp = int(148 / (blocks < 1 ? 1 : blocks));
+    if (sp > p.n_tiles / 4) sp = p.n_tiles / 4;
+    if (sp < 1) sp = 1;
+    p.split_tiles = (p.n_tiles + sp - 1) / sp;
+    p.n_splits = (p.n_tiles + p.split_tiles - 1) / p.split_tiles;
+    size_t off = kWsHeader;
+    auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) & ~size_t(255); return o; };
+    p.off_meta = take(size_t(p.round) * p.n_tiles * sizeof(TileMeta));
+    p.off_img = take(size_t(p.round) * pair_bytes);
+    const size_t rows = size_t(s.total_q) * s.Hq * p.n_splits;
+    p.off_po = take(p.n_splits > 1 ? rows * L.d * 4 : 0);
+    p.off_pml = take(p.n_splits > 1 ? rows * 8 : 0);
+    p.total = off;
+    return p;
+}
+
+template <int D>
+int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
+           const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, cudaStream_t st) {
+    const TcPlan p = tc_plan(L, s);
+    cudaError_t e = cudaFuncSetAttribute(cross_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(expand_smem<D>()));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(cross_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(attend_smem<D>()));
+    if (e != cudaSuccess) return e;
+    ExpandArgs x{};
+    x.L = L;
+    x.kp = kp->dev;
+    x.vp = vp->dev;
+    x.table = s.block_table;
+    x.kv_lens = s.kv_lens;
+    x.bt_stride = s.max_blocks;
+    x.max_kv_len = s.max_kv_len;
+    x.cache = cache;
+    x.num_blocks = num_blocks;
+    x.n_tiles = p.n_tiles;
+    x.images = ws + p.off_img;
+    x.meta = reinterpret_cast<TileMeta *>(ws + p.off_meta);
+    x.status = reinterpret_cast<uint32_t *>(ws);
+    AttendArgs a{};
+    a.Q = static_cast<const __nv_bfloat16 *>(Q);
+    a.Hq = s.Hq;
+    a.H = L.H;
+    a.G = s.Hq / L.H;
+    a.PT = kTile / a.G;
+    a.cu_q = s.cu_q;
+    a.kv_lens = s.kv_lens;
+    a.total_q = s.total_q;
+    a.max_q = s.max_q;
+    a.max_kv_len = s.max_kv_len;
+    a.n_tiles = p.n_tiles;
+    a.images = x.images;
+    a.meta = x.meta;
+    a.ksigns = kp->dev.signs;
+    a.vsigns = vp->dev.signs;
+    a.n_splits = p.n_splits;
+    a.split_tiles = p.split_tiles;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse;
+    a.part_o = reinterpret_cast<float *>(ws + p.off_po);
+    a.part_ml = reinterpret_cast<float *>(ws + p.off_pml);
+    a.status = x.status;
+    for (int p0 = 0; p0 < p.pairs; p0 += p.round) {
+        const int np = p.pairs - p0 < p.round ? p.pairs - p0 : p.round;
+        x.pair0 = a.pair0 = p0;
+        x.n_pairs = np;
+        const int64_t items = int64_t(np) * p.n_tiles;
+        cross_expand_kernel<D><<<unsigned(items < 296 ? items : 296), 256, expand_smem<D>(), st>>>(x);
+        cross_attend_kernel<D><<<dim3(unsigned(p.x), unsigned(np), unsigned(p.n_splits)), kAttendThreads,
+                                 attend_smem<D>(), st>>>(a);
+        if (p.n_splits > 1)
+            cross_merge_kernel<D><<<dim3(unsigned((int64_t(s.max_q) * a.G + 3) / 4), unsigned(np)), 128, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool cross_tc_covers(const Layout &L, bool dense, const CrossShape &s) {
+    if ((L.d != 64 && L.d != 128) || dense) return false;
+    return s.max_q > 4;
+}
+
+size_t cross_tc_ws_bytes(const Layout &L, const CrossShape &s) { return tc_plan(L, s).total; }
+
+int launch_cross_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
+                    const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, cudaStream_t st) {
+    if (L.d == 128) return run_tc<128>(kp, vp, L, Q, s, cache, num_blocks, out, lse, ws, st);
+    return run_tc<64>(kp, vp, L, Q, s, cache, num_blocks, out, lse, ws, st);
+}
+
+}  // namespace tq

@@ -242,6 +242,13 @@ size_t cross_ws_bytes(const Layout &L, const CrossShape &s);
 int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
                  const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream);
 
+// The tensor-core path (head sizes 64 and 128, Hadamard rotations): whether
+// it is taken, its workspace (header included), its launcher.
+bool cross_tc_covers(const Layout &L, bool dense, const CrossShape &s);
+size_t cross_tc_ws_bytes(const Layout &L, const CrossShape &s);
+int launch_cross_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
+                    const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, cudaStream_t st);
+
 // Pages of a cache (arguments checked by the caller).
 size_t pages_ws_bytes(int64_t num_blocks, int n_rows, int max_blocks);
 int launch_pages_reserve(const Layout &L, const tq_page_pool &pool, const int32_t *new_tokens, int32_t *slots,
