@@ -55,6 +55,32 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// Packed pairs of fp32 (one issue slot for two operations).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                  "r"(tc05::smem_u32(src)), "r"(bytes)
@@ -71,8 +97,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
-// Bounded wait (about a second) that also gives up once another thread has.
+// Bounded wait (a second or more) that also gives up once another thread has.
+// The first polls name no time to sleep: a thread woken from a long sleep
+// came back some 500 cycles late.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag) {
+    for (uint32_t i = 0; i < 256u; ++i)
+        if (tc05::mbar_test_wait(bar, parity)) return true;
     for (uint32_t i = 0; i < 500000u; ++i) {
         if (tc05::mbar_try_wait_sleep(bar, parity, 2000u)) return true;
         if ((i & 63u) == 63u && *abort_flag) return false;
@@ -401,7 +431,12 @@ template <int D>
 constexpr size_t attend_smem() {
     return (2 + ring_slots<D>()) * image_bytes(D) + kMetaSlots * sizeof(TileMeta) + kBarBytes + 1024;
 }
-constexpr int kAttendThreads = 320;        // two tiles of softmax rows, the MMA issuer's warp, the loader's
+// Three warpgroups: two of softmax rows, one with the MMA issuer's warp and
+// the loader's.  The first two take registers that the third gives up
+// (168 x 3 = 232 x 2 + 40): a row's 128 logits stay in registers.
+constexpr int kAttendThreads = 384;
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
 
 template <int D>
 __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const __grid_constant__ AttendArgs a) {
@@ -420,7 +455,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     const int tile0 = split * a.split_tiles;
     const int n = min((len + kTile - 1) / kTile - tile0, a.split_tiles);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const int tt = (tid >> 7) & 1, r = tid & 127;         // softmax threads: query tile and row
     const int qpos = pos0 + tt * a.PT + r / a.G;
     const bool row_ok = tid < 256 && r < a.PT * a.G && qpos < nq;
@@ -451,10 +486,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     uint64_t *kv_empty = bars + 8;                        // [NS] its products done (commit)
     uint64_t *meta_full = bars + 16;                      // [8]
     uint64_t *s_full = bars + 24;                         // [2] S of a query tile done (commit)
-    uint64_t *p_full = bars + 26;                         // [2] P written, O rescaled (128)
-    uint64_t *o_done = bars + 28;                         // [2] last product of a tile done (commit)
-    uint64_t *q_full = bars + 30;                         // queries staged (128 a tile)
-    uint64_t *drained = bars + 31;                        // products in flight when a wait gave up
+    uint64_t *p_half = bars + 26;                         // [2] first 64 keys of P written, O rescaled (a lane of 4 warps)
+    uint64_t *p_full = bars + 28;                         // [2] the rest
+    uint64_t *o_done = bars + 30;                         // [2] last product of a tile done (commit)
+    uint64_t *q_full = bars + 32;                         // queries staged (4 warps a tile)
+    uint64_t *drained = bars + 33;                        // products in flight when a wait gave up
     volatile uint32_t *abort_flag = &abort_word;
     if (warp == 8) {
         tc05::tmem_alloc(&tmem_holder, 512);
@@ -468,10 +504,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
         for (int i = 0; i < kMetaSlots; ++i) tc05::mbar_init(&meta_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             tc05::mbar_init(&s_full[i], 1);
-            tc05::mbar_init(&p_full[i], 128);
+            tc05::mbar_init(&p_half[i], 4);
+            tc05::mbar_init(&p_full[i], 4);
             tc05::mbar_init(&o_done[i], 1);
         }
-        tc05::mbar_init(q_full, uint32_t(128 * n_t));
+        tc05::mbar_init(q_full, uint32_t(4 * n_t));
         tc05::mbar_init(drained, 1);
         abort_word = 0u;
         tc05::fence_mbar_init();
@@ -482,6 +519,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     const uint32_t tmem = tmem_holder;
     bool timeout = false;
 
+    if (warp >= 8) {
+        fewer_registers();
     if (warp == 9) {
         // ================= loader: K(0), V(0), K(1), V(1), ... through one ring
         if (lane == 0) {
@@ -515,64 +554,98 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
         }
         __syncwarp();
     } else if (warp == 8) {
-        // ================= MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = tc05::idesc_f16_f32(128, 128);
-            constexpr uint32_t idesc_pv = tc05::idesc_f16_f32(128, D) | tc05::kIdescBMajorMN;
-            const uint32_t q_s = tc05::smem_u32(sQ), ring_s = tc05::smem_u32(ring);
-            auto landed = [&](int i) { return wait_or_abort(&kv_full[i % NS], uint32_t(i / NS) & 1u, abort_flag); };
-            auto qk = [&](int t, int i) {                  // S_t = Q_t K^T, K in ring entry i
-                const uint32_t A = q_s + uint32_t(t) * kImg, B = ring_s + uint32_t(i % NS) * kImg;
+        // ================= MMA issuer: the whole warp walks the loop, so that
+        // addresses and descriptors stay in uniform registers, and one lane
+        // issues (a single lane's own loop took 70 to 115 cycles a product,
+        // more than the 64 that it runs)
+        constexpr uint32_t idesc_qk = tc05::idesc_f16_f32(128, 128);
+        constexpr uint32_t idesc_pv = tc05::idesc_f16_f32(128, D) | tc05::kIdescBMajorMN;
+        const bool lead = elect_one();
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        const uint64_t dq = tc05::desc_kmajor_sw128(tc05::smem_u32(sQ));
+        const uint64_t dk = tc05::desc_kmajor_sw128(tc05::smem_u32(ring));
+        const uint64_t dv = tc05::desc_mnmajor_sw128(tc05::smem_u32(ring), 16384u, 1024u);
+        auto wait_w = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(kFull, wait_or_abort(bar, parity, abort_flag));
+        };
+        auto qk = [&](int t, int slot) {                   // S_t = Q_t K^T, K in a ring slot
+            const uint64_t A = dq + uint64_t(t) * (kImg >> 4), B = dk + uint64_t(slot) * (kImg >> 4);
+            const uint32_t S = tm + uint32_t(t) * 128u;
+            if (lead) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u;
-                    tc05::mma_f16(tmem + uint32_t(t) * 128u, tc05::desc_kmajor_sw128(A + o), tc05::desc_kmajor_sw128(B + o),
-                                  idesc_qk, ks > 0);
+                    const uint32_t o = (uint32_t(ks >> 2) * 16384u + uint32_t(ks & 3) * 32u) >> 4;
+                    tc05::mma_f16(S, A + o, B + o, idesc_qk, ks > 0);
                 }
                 tc05::mma_commit(&s_full[t]);
-            };
-            auto pv = [&](int t, int i, bool add) {        // O_t += P_t V, V in ring entry i
-                const uint32_t B = ring_s + uint32_t(i % NS) * kImg;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc05::mma_f16_ts(tmem + TO + uint32_t(t * D), tmem + uint32_t(t) * 128u + uint32_t(ks) * 8u,
-                                     tc05::desc_mnmajor_sw128(B + uint32_t(ks) * 2048u, 16384u, 1024u), idesc_pv,
-                                     add || ks > 0);
-            };
-            int started = 0;                               // s_full commits per tile so far (all tiles alike)
-            bool ok = wait_or_abort(q_full, 0u, abort_flag) && landed(0);
-            if (ok) {
-                tc05::fence_after_sync();
-                for (int t = 0; t < n_t; ++t) qk(t, 0);
-                tc05::mma_commit(&kv_empty[0]);
-                started = 1;
             }
-            for (int j = 0; j < n && ok; ++j) {
-                ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
-                for (int t = 0; t < n_t && ok; ++t) {
-                    ok = wait_or_abort(&p_full[t], uint32_t(j) & 1u, abort_flag);
-                    if (!ok) break;
-                    tc05::fence_after_sync();
-                    pv(t, 2 * j + 1, j > 0);
-                    if (t == n_t - 1) tc05::mma_commit(&kv_empty[(2 * j + 1) % NS]);
-                    if (j + 1 < n) {
-                        // in issue order behind the product that reads P from the same columns
-                        qk(t, 2 * j + 2);
-                        if (t == n_t - 1) tc05::mma_commit(&kv_empty[(2 * j + 2) % NS]);
-                    } else {
-                        tc05::mma_commit(&o_done[t]);
-                    }
+        };
+        auto pv = [&](int t, int slot, int half, bool add) {   // O_t += P_t V over 64 keys, V in a ring slot
+            const uint64_t B = dv + uint64_t(slot) * (kImg >> 4) + uint64_t(half) * (8192u >> 4);
+            const uint32_t P = tm + uint32_t(t) * 128u + uint32_t(half) * 32u, O = tm + TO + uint32_t(t * D);
+            if (lead) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc05::mma_f16_ts(O, P + uint32_t(ks) * 8u, B + uint32_t(ks) * (2048u >> 4), idesc_pv, add || ks > 0);
+            }
+        };
+        auto release = [&](uint64_t *bar) {
+            if (lead) tc05::mma_commit(bar);
+        };
+        int slot = 0;                                      // ring slot and phase of the next operand tile
+        uint32_t phase = 0;
+        auto next = [&](int *at) {                         // waits for it
+            *at = slot;
+            const bool ok = wait_w(&kv_full[slot], phase);
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1u;
+            }
+            return ok;
+        };
+        int k_slot = 0, v_slot = 0;
+        bool started = false;
+        bool ok = wait_w(q_full, 0u) && next(&k_slot);
+        if (ok) {
+            tc05::fence_after_sync();
+            for (int t = 0; t < n_t; ++t) qk(t, k_slot);
+            release(&kv_empty[k_slot]);
+            started = true;
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            ok = next(&v_slot) && (!more || next(&k_slot));
+            for (int t = 0; t < n_t && ok; ++t) {
+                const bool last = t == n_t - 1;
+                ok = wait_w(&p_half[t], uint32_t(j) & 1u);
+                if (!ok) break;
+                tc05::fence_after_sync();
+                pv(t, v_slot, 0, j > 0);
+                ok = wait_w(&p_full[t], uint32_t(j) & 1u);
+                if (!ok) break;
+                tc05::fence_after_sync();
+                pv(t, v_slot, 1, true);
+                if (last) release(&kv_empty[v_slot]);
+                if (more) {
+                    // in issue order behind the product that reads P from the same columns
+                    qk(t, k_slot);
+                    if (last) release(&kv_empty[k_slot]);
+                } else {
+                    release(&o_done[t]);
                 }
             }
-            timeout = !ok;
-            if (timeout && started) {
-                // what was issued completes before TMEM and shared memory are given back
-                tc05::mma_commit(drained);
-                wait_bounded(drained, 0u);
-            }
+        }
+        timeout = !ok;
+        if (timeout && started) {
+            // what was issued completes before TMEM and shared memory are given back
+            release(drained);
+            wait_bounded(drained, 0u);
         }
         __syncwarp();
-    } else if (tt < n_t) {
+    }
+    } else {
+        more_registers();
+    if (tt < n_t) {
         // ================= softmax: a thread per query row
         const uint32_t lrow = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lrow + uint32_t(tt) * 128u, to = tmem + lrow + TO + uint32_t(tt * D);
@@ -616,7 +689,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
                                h2u(x[8 * c + 4] * down, x[8 * c + 5] * down), h2u(x[8 * c + 6] * down, x[8 * c + 7] * down));
         }
         tc05::fence_proxy_async_smem();
-        tc05::mbar_arrive(q_full);
+        __syncwarp();
+        if (lane == 0) tc05::mbar_arrive(q_full);
         // waits decided per warp, so the warp-wide TMEM accesses stay converged
         auto wait_w = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(kFull, wait_or_abort(bar, parity, abort_flag));
@@ -644,7 +718,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             }
             float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int i = 4; i < 128; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
+            for (int i = 4; i < 124; i += 8)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(mx4[u], fmaxf(s[i + 2 * u], s[i + 2 * u + 1]));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(mx4[u], s[124 + u]);
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             const float c2 = fmaxf(rowc * sc.x, 1e-37f);
             const float top = fmaf(mx, c2, sc.y);
@@ -669,24 +747,29 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
                 }
             }
             const float off = m == -INFINITY ? 0.f : sc.y - m;
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float p0 = ex2_approx(fmaf(s[c * 32 + 2 * e], c2, off));
-                    const float p1 = ex2_approx(fmaf(s[c * 32 + 2 * e + 1], c2, off));
-                    sum4[(2 * e) & 3] += p0;
-                    sum4[(2 * e + 1) & 3] += p1;
-                    p[e] = h2u(p0, p1);
+                    const float2 x = fma2(make_float2(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), c22, off2);
+                    const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    sum[e & 1] = add2(sum[e & 1], w);
+                    p[e] = h2u(w.x, w.y);
                 }
                 tc05::tmem_st_32x32b_x16(ts + uint32_t(c * 16), p);
+                if (c & 1) {
+                    // 64 keys: their product may start.  One lane arrives for its
+                    // warp: 128 arrivals on one barrier took some 400 cycles
+                    tc05::tmem_wait_st();
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc05::mbar_arrive(c == 1 ? &p_half[tt] : &p_full[tt]);
+                }
             }
-            l = fmaf((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]), sc.z, l);
-            tc05::tmem_wait_st();
-            tc05::fence_before_sync();
-            tc05::mbar_arrive(&p_full[tt]);
+            l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), sc.z, l);
         }
         if (!timeout && !wait_w(&o_done[tt], 0u)) timeout = true;
         tc05::fence_after_sync();
@@ -720,6 +803,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             }
             if (a.lse) a.lse[row] = l != l ? l : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
+    }
     }
     tc05::fence_before_sync();
     __syncthreads();
