@@ -10,9 +10,9 @@
 //            bases as fp16 operand tiles in the workspace, laid out as the
 //            tensor cores read them from shared memory.  S^T s is a product of
 //            +-1 signs (exact) with S as fp16 (exact for |S| >= 2^-14) on
-//            tcgen05.  A tile is scaled by a power of two to a largest
-//            magnitude in [2^10, 2^11), so keys of any norm keep fp16's 11
-//            bits down to 2^-25 of the tile's largest coordinate.
+//            tcgen05.  A tile is scaled by a power of two that brings a bound on
+//            its coordinates (from its largest norm) to [2^14, 2^15), so states
+//            of any norm keep fp16's 11 bits down to 2^-28 of that bound.
 //   attend   256 query rows (two tiles of 128 rows: positions x heads of the
 //            group) walk the tiles: S = Q K^T and O += P V on tcgen05, the
 //            online softmax between them, a thread per row.
@@ -122,65 +122,121 @@ struct ExpandArgs {
     const uint8_t *cache;
     int64_t num_blocks;
     int pair0, n_pairs, n_tiles;           // pairs (sequence, KV head) of this launch
+    int32_t *order;                        // [n_pairs] see order_pairs
+    int B;
     uint8_t *images;                       // [pair][tile][keys | values]
     TileMeta *meta;                        // [pair][tile]
     uint32_t *status;
 };
 
-struct CodeTables {
-    float lv[16], lv2[8], polar[132];
+// A thread's half of a token's codes (keys or values): where they are and how
+// wide.  A fractional rate has an array and a codebook for each half.
+struct HalfCode {
+    int off, bpt, hoff, hbpt;              // array of fields, 3-bit codes' sign bits
+    int width;                             // 1, 2, 4 bits; 8: E4M3; 0: polar
+    bool signs;
+    const float *lv;                       // levels by code (shared memory)
 };
 
-// Eight coordinates (8 cc ..) of a token's reconstruction without its norm.
-template <int D>
-__device__ __forceinline__ void levels8(const CodeTables &tab, const uint8_t *page, int pos, int cc, bool polar,
-                                        bool fp8, bool half, int a_bits, int b_bits, int off, int bpt, int w, int hoff,
-                                        int hbpt, int off2, int bpt2, int w2, int hoff2, int hbpt2, float (&y)[8]) {
-    if (polar) {
+// coord(i, y) for the thread's D / 2 coordinates, without their norm.
+template <int D, int W, bool SIGNS, typename F>
+__device__ __forceinline__ void walk_codes(const HalfCode &hc, const uint8_t *page, int pos, F &&chunk) {
+    constexpr int HALF = D / 2, BYTES = HALF * W / 8, WORDS = BYTES < 4 ? 1 : BYTES / 4;
+    uint32_t w[WORDS], sg[HALF / 32];
+    const uint8_t *at = page + hc.off + pos * hc.bpt;
+    if constexpr (BYTES >= 16) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float2 v = polar_pair<D>(page + off + pos * bpt, page + off2 + pos * bpt2, tab.polar, 4 * cc + p);
-            y[2 * p] = v.x;
-            y[2 * p + 1] = v.y;
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(at)[i];
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
-        return;
-    }
-    const bool second = half && cc >= D / 16;
-    const int c = second ? cc - D / 16 : cc;
-    const int width = second ? w2 : w;
-    const uint8_t *at = page + (second ? off2 + pos * bpt2 : off + pos * bpt) + c * width;
-    if (fp8) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(at);
-        const float s = rsqrtf(float(D));
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = s * e4m3_to_float(uint8_t((e < 4 ? v.x : v.y) >> (8 * (e & 3))));
-        return;
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(at)[i];
     }
-    uint32_t bits;
-    if (width == 4) bits = *reinterpret_cast<const uint32_t *>(at);
-    else if (width == 2) bits = *reinterpret_cast<const uint16_t *>(at);
-    else bits = *at;
-    uint32_t high = 0;
-    if ((second ? b_bits : a_bits) == 3) high = page[(second ? hoff2 + pos * hbpt2 : hoff + pos * hbpt) + c];
-    const float *lv = second ? tab.lv2 : tab.lv;
-    const uint32_t m = (1u << width) - 1u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = lv[((bits >> (e * width)) & m) | (((high >> e) & 1u) << 2)];
+    for (int i = 0; i < HALF / 32; ++i)
+        sg[i] = SIGNS ? reinterpret_cast<const uint32_t *>(page + hc.hoff + pos * hc.hbpt)[i] : 0u;
+#pragma unroll
+    for (int c = 0; c < HALF / 8; ++c) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = c * 8 + e;
+            if constexpr (W == 8) {
+                y[e] = e4m3_to_float(uint8_t(w[i >> 2] >> (8 * (i & 3))));
+            } else {
+                uint32_t k = (w[i * W / 32] >> (i * W % 32)) & ((1u << W) - 1u);
+                if (SIGNS) k |= ((sg[i >> 5] >> (i & 31)) & 1u) << 2;
+                y[e] = hc.lv[k];
+            }
+        }
+        chunk(c, y);
+    }
+}
+template <int D, typename F>
+__device__ __forceinline__ void walk(const HalfCode &hc, const uint8_t *page, int pos, int hh, int off2, int bpt2,
+                                     const float *polar, F &&chunk) {
+    switch (hc.width) {
+        case 4: walk_codes<D, 4, false>(hc, page, pos, chunk); break;
+        case 2:
+            if (hc.signs) walk_codes<D, 2, true>(hc, page, pos, chunk);
+            else walk_codes<D, 2, false>(hc, page, pos, chunk);
+            break;
+        case 1: walk_codes<D, 1, false>(hc, page, pos, chunk); break;
+        case 8: walk_codes<D, 8, false>(hc, page, pos, chunk); break;
+        default:
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                float y[8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float2 v = polar_pair<D>(page + hc.off + pos * hc.bpt, page + off2 + pos * bpt2, polar,
+                                                   hh * (D / 4) + 4 * c + p);
+                    y[2 * p] = v.x;
+                    y[2 * p + 1] = v.y;
+                }
+                chunk(c, y);
+            }
+    }
 }
 
 template <int D>
 constexpr size_t expand_smem() { return size_t(D) * D * 2 + 2 * image_bytes(D) + 1024; }
 
-// Power-of-two scale of a tile from its largest magnitude; *e: value = stored * 2^e.
-__device__ __forceinline__ float tile_scale(float mx, int *e) {
-    int ex = 11;
+// Power of two that brings mx to [2^(top - 1), 2^top); *e: value = stored * 2^e.
+__device__ __forceinline__ float scale_to(float mx, int top, int *e) {
+    int ex = top;
     if (mx > 0.f && mx < INFINITY) frexpf(mx, &ex);
-    *e = ex - 11;
-    return ldexpf(1.f, 11 - ex);
+    *e = ex - top;
+    return ldexpf(1.f, top - ex);
+}
+
+// The pairs of the launch, those of long sequences first, for the attention's
+// blocks: with the longest last, their blocks ran on alone (8 runs of 1,024
+// over 1 to 8,192 states: 586 us unsorted).  Ranks by counting, up to
+// kMaxOrder sequences (there are enough blocks to even out beyond that) and
+// only where one launch has every pair.
+constexpr int kMaxOrder = 512;
+__device__ void order_pairs(const ExpandArgs &a) {
+    const bool sort = a.B <= kMaxOrder && a.n_pairs == a.B * a.L.H;
+    for (int p = threadIdx.x; p < a.n_pairs; p += blockDim.x) {
+        int to = p;
+        if (sort) {
+            const int b = p / a.L.H, len = a.kv_lens[b];
+            int before = 0;
+            for (int c = 0; c < a.B; ++c) before += a.kv_lens[c] > len || (a.kv_lens[c] == len && c < b);
+            to = before * a.L.H + p % a.L.H;
+        }
+        a.order[to] = p;
+    }
 }
 
 // Persistent over (pair, tile); 256 threads, thread (key, half of its
-// coordinates).
+// coordinates): one table lookup and a product a value, one more for a key's
+// sketch.  (Kept in fp32 registers until the tile's true maximum was known, and
+// with the codec looked at in every chunk, it took four times the
+// instructions: 130 us instead of 39 for 2,600 tiles at d = 128.)
 template <int D>
 __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int HALF = D / 2, NC = D / 16;          // coordinates and 16-byte chunks of a thread
@@ -188,14 +244,16 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_holder;
     __shared__ __align__(8) uint64_t bar;
-    __shared__ float red[2][8];
-    __shared__ CodeTables tk, tv;
+    __shared__ float red[2][2][8];
+    __shared__ float lv[4][16], polar[2][132];
+    __shared__ float bound[2];                        // of a coordinate over the vector's norm
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sS = sm, *sK = sm + D * D * 2, *sV = sK + kImg;
     const Layout &L = a.L;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int key = tid & 127, hh = tid >> 7;
 
+    if (blockIdx.x == 0) order_pairs(a);
     // S as the B operand: row j holds S[j][0 .. D), 64 columns to a half
     if (L.kqjl)
         for (int i = tid; i < D * D / 8; i += 256) {
@@ -203,17 +261,17 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
             *reinterpret_cast<uint4 *>(sS + (c >> 3) * (D * 128) + tc05::sw128_offset(uint32_t(j), uint32_t(c & 7))) =
                 *reinterpret_cast<const uint4 *>(a.kp.S16 + size_t(j) * D + c * 8);
         }
-    if (tid < 16) {
-        tk.lv[tid] = (L.ka_bits <= 4 && tid < (1 << L.ka_bits)) ? a.kp.lv[tid] : 0.f;
-        tv.lv[tid] = (L.va_bits <= 4 && tid < (1 << L.va_bits)) ? a.vp.lv[tid] : 0.f;
-        if (tid < 8) {
-            tk.lv2[tid] = (L.khalf && tid < (1 << L.kb_bits)) ? a.kp.lv2[tid] : 0.f;
-            tv.lv2[tid] = (L.vhalf && tid < (1 << L.vb_bits)) ? a.vp.lv2[tid] : 0.f;
-        }
+    // levels: keys' first and second codebook, values' first and second
+    if (tid < 64) {
+        const int i = tid & 15, which = tid >> 4;
+        const DevParams &P = which < 2 ? a.kp : a.vp;
+        const int bits = which == 0 ? L.ka_bits : which == 1 ? L.kb_bits : which == 2 ? L.va_bits : L.vb_bits;
+        const float *src = (which & 1) ? ((which == 1 ? L.khalf : L.vhalf) ? P.lv2 : nullptr) : bits <= 4 ? P.lv : nullptr;
+        lv[which][i] = src && i < (1 << bits) ? src[i] : 0.f;
     }
     for (int i = tid; i < 132; i += 256) {
-        tk.polar[i] = L.kpolar ? a.kp.polar[i] : 0.f;
-        tv.polar[i] = L.vpolar ? a.vp.polar[i] : 0.f;
+        polar[0][i] = L.kpolar ? a.kp.polar[i] : 0.f;
+        polar[1][i] = L.vpolar ? a.vp.polar[i] : 0.f;
     }
     if (warp == 0) {
         tc05::tmem_alloc(&tmem_holder, D);
@@ -227,8 +285,32 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
+    if (tid < 2) {
+        float mx = 0.f;
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(lv[2 * tid + (i >> 4)][i & 15]));
+        if (tid == 0 && L.kbits == 8) mx = 448.f * rsqrtf(float(D));
+        if (tid == 0 ? L.kpolar : L.vpolar) mx = 1.f;
+        bound[tid] = mx;
+    }
+    __syncthreads();
     const uint32_t tmem = tmem_holder, lrow = uint32_t((warp & 3) * 32) << 16;
     const float cq = 1.2533141373155003f / float(D);   // sqrt(pi/2) / m
+    const bool k2 = L.khalf && hh, v2 = L.vhalf && hh; // this half has arrays of its own
+    HalfCode kc, vc;
+    kc.width = L.kpolar ? 0 : k2 ? L.kc2_w : L.kc_w;
+    kc.off = k2 ? L.kc2_off : L.kc_off + (L.khalf || L.kpolar ? 0 : hh * HALF * L.kc_w / 8);
+    kc.bpt = k2 ? L.kc2_bpt : L.kc_bpt;
+    kc.signs = (k2 ? L.kb_bits : L.ka_bits) == 3;
+    kc.hoff = k2 ? L.kh2_off : L.kh_off + (L.khalf ? 0 : hh * HALF / 8);
+    kc.hbpt = k2 ? L.kh2_bpt : L.kh_bpt;
+    kc.lv = lv[k2 ? 1 : 0];
+    vc.width = L.vpolar ? 0 : v2 ? L.vc2_w : L.vc_w;
+    vc.off = v2 ? L.vc2_off : L.vc_off + (L.vhalf || L.vpolar ? 0 : hh * HALF * L.vc_w / 8);
+    vc.bpt = v2 ? L.vc2_bpt : L.vc_bpt;
+    vc.signs = (v2 ? L.vb_bits : L.va_bits) == 3;
+    vc.hoff = v2 ? L.vh2_off : L.vh_off + (L.vhalf ? 0 : hh * HALF / 8);
+    vc.hbpt = v2 ? L.vh2_bpt : L.vh_bpt;
+    vc.lv = lv[v2 ? 3 : 2];
     uint32_t phase = 0;
     bool timeout = false;
 
@@ -238,30 +320,56 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         const int pair = a.pair0 + pl, b = pair / L.H, h = pair - b * L.H;
         const int len = min(max(a.kv_lens[b], 0), a.max_kv_len);
         if (tile * kTile >= len) continue;
-        if (tid == 0) bulk_wait_read();                // the tiles of the item before have been read
-        __syncthreads();
         const int t = tile * kTile + key, pos = t % L.P;
         const uint8_t *page = nullptr;
+        float nk = 0.f, nv = 0.f, rk = 0.f;
         if (t < len) {
             const int blk = a.table[int64_t(b) * a.bt_stride + t / L.P];
-            if (blk >= 0 && blk < a.num_blocks) page = a.cache + (int64_t(blk) * L.H + h) * int64_t(L.page_bytes);
-            else atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
+            if (blk >= 0 && blk < a.num_blocks) {
+                page = a.cache + (int64_t(blk) * L.H + h) * int64_t(L.page_bytes);
+                nk = h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kn_off + pos * 2));
+                nv = h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.vn_off + pos * 2));
+                if (L.kqjl) rk = cq * h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kr_off + pos * 2));
+            } else {
+                atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
+            }
         }
+        if (tid == 0) bulk_wait_read();                // the tiles of the item before have been read
+        // a key's coordinate is below bound nk + rk sum_j |S_ji|, and |S_ji| below
+        // 8.6 (Box-Muller of 53-bit uniforms)
+        const float kmx = warp_max(fmaf(fabsf(rk), 8.6f * D, fabsf(nk) * bound[0])), vmx = warp_max(fabsf(nv) * bound[1]);
+        if (lane == 0) {
+            red[0][phase & 1][warp] = kmx;
+            red[1][phase & 1][warp] = vmx;
+        }
+        __syncthreads();
+        float km = 0.f, vm = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            km = fmaxf(km, red[0][phase & 1][i]);
+            vm = fmaxf(vm, red[1][phase & 1][i]);
+        }
+        int ek, ev;
+        const float ksc = scale_to(km, 15, &ek), vsc = scale_to(vm, 15, &ev);
+        auto at = [&](uint8_t *img, int c) {           // the thread's chunk c of its key's row
+            const int cc = hh * NC + c;
+            return reinterpret_cast<uint4 *>(img + (cc >> 3) * 16384 + tc05::sw128_offset(uint32_t(key), uint32_t(cc & 7)));
+        };
         if (L.kqjl) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int cc = hh * NC + c;
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (page) {
-                    const uint32_t bits = page[L.ks_off + pos * L.ks_bpt + cc];
+            for (int c = 0; c < NC; c += 4) {
+                const uint32_t bits =
+                    page ? *reinterpret_cast<const uint32_t *>(page + L.ks_off + pos * L.ks_bpt + hh * (HALF / 8) + c) : 0u;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {      // +1 where the bit is set, else -1
-                        const uint32_t u = bits >> (2 * q);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {      // +1 where the bit is set, else -1 (a missing key's row is not used)
+                        const uint32_t u = bits >> (8 * k + 2 * q);
                         w[q] = 0xBC00BC00u ^ (((u << 15) & 0x8000u) | ((u << 30) & 0x80000000u));
                     }
+                    *at(sK, c + k) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *reinterpret_cast<uint4 *>(sK + (cc >> 3) * 16384 + tc05::sw128_offset(uint32_t(key), uint32_t(cc & 7))) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
             }
             tc05::fence_proxy_async_smem();
             tc05::fence_before_sync();
@@ -279,80 +387,46 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
             }
         }
         // values, while the product runs
-        float y[HALF], mx = 0.f;
-        const float nv = page ? h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.vn_off + pos * 2)) : 0.f;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        if (page) {
+            const float f = nv * vsc;
+            walk<D>(vc, page, pos, hh, L.vc2_off, L.vc2_bpt, polar[1], [&](int c, const float (&y)[8]) {
+                *at(sV, c) = make_uint4(h2u(y[0] * f, y[1] * f), h2u(y[2] * f, y[3] * f), h2u(y[4] * f, y[5] * f),
+                                        h2u(y[6] * f, y[7] * f));
+            });
+        } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (page)
-                levels8<D>(tv, page, pos, hh * NC + c, L.vpolar, false, L.vhalf, L.va_bits, L.vb_bits, L.vc_off, L.vc_bpt,
-                           L.vc_w, L.vh_off, L.vh_bpt, L.vc2_off, L.vc2_bpt, L.vc2_w, L.vh2_off, L.vh2_bpt, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[c * 8 + e] = nv * v[e];
-                mx = fmaxf(mx, fabsf(y[c * 8 + e]));
-            }
+            for (int c = 0; c < NC; ++c) *at(sV, c) = zero;
         }
-        mx = warp_max(mx);
-        if (lane == 0) red[0][warp] = mx;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[0][i]);
-        int ev;
-        float sc = tile_scale(mx, &ev);
-        auto store = [&](uint8_t *img) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int cc = hh * NC + c;
-                *reinterpret_cast<uint4 *>(img + (cc >> 3) * 16384 + tc05::sw128_offset(uint32_t(key), uint32_t(cc & 7))) =
-                    make_uint4(h2u(y[c * 8] * sc, y[c * 8 + 1] * sc), h2u(y[c * 8 + 2] * sc, y[c * 8 + 3] * sc),
-                               h2u(y[c * 8 + 4] * sc, y[c * 8 + 5] * sc), h2u(y[c * 8 + 6] * sc, y[c * 8 + 7] * sc));
-            }
-        };
-        store(sV);
-        // keys
-        const float nk = page ? h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kn_off + pos * 2)) : 0.f;
-        const float rk = page && L.kqjl ? cq * h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kr_off + pos * 2)) : 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (page)
-                levels8<D>(tk, page, pos, hh * NC + c, L.kpolar, L.kbits == 8, L.khalf, L.ka_bits, L.kb_bits, L.kc_off,
-                           L.kc_bpt, L.kc_w, L.kh_off, L.kh_bpt, L.kc2_off, L.kc2_bpt, L.kc2_w, L.kh2_off, L.kh2_bpt, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[c * 8 + e] = nk * v[e];
-        }
+        bool ok = true;
         if (L.kqjl) {
-            const bool ok = __all_sync(kFull, wait_bounded(&bar, phase & 1u));
-            timeout = !ok;
-            ++phase;
+            ok = __all_sync(kFull, wait_bounded(&bar, phase & 1u));
             tc05::fence_after_sync();
-            if (ok) {
-#pragma unroll
-                for (int c = 0; c < HALF / 32; ++c) {
-                    uint32_t r[32];
-                    tc05::tmem_ld_32x32b_x32(tmem + lrow + uint32_t(hh * HALF + c * 32), r);
-                    tc05::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[c * 32 + e] = fmaf(rk, __uint_as_float(r[e]), y[c * 32 + e]);
-                }
-            }
         }
-        mx = 0.f;
+        ++phase;
+        // keys: the thread's part of the product comes 32 coordinates at a time
+        uint32_t r[HALF];
+        if (L.kqjl) {
 #pragma unroll
-        for (int e = 0; e < HALF; ++e) mx = fmaxf(mx, fabsf(y[e]));
-        mx = warp_max(mx);
-        if (lane == 0) red[1][warp] = mx;
-        const bool out_of_time = __syncthreads_or(timeout);   // also: every thread has its part of the product
-        if (out_of_time) {
-            timeout = true;
-            break;
+            for (int c = 0; c < HALF / 32; ++c)
+                tc05::tmem_ld_32x32b_x32(tmem + lrow + uint32_t(hh * HALF + c * 32), reinterpret_cast<uint32_t(&)[32]>(r[c * 32]));
+            tc05::tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) r[i] = 0u;
         }
+        if (page) {
+            const float f = nk * ksc * (L.kbits == 8 ? rsqrtf(float(D)) : 1.f), g = rk * ksc;
+            walk<D>(kc, page, pos, hh, L.kc2_off, L.kc2_bpt, polar[0], [&](int c, const float (&y)[8]) {
+                float k[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[1][i]);
-        int ek;
-        sc = tile_scale(mx, &ek);
-        store(sK);
+                for (int e = 0; e < 8; ++e) k[e] = fmaf(g, __uint_as_float(r[c * 8 + e]), y[e] * f);
+                *at(sK, c) = make_uint4(h2u(k[0], k[1]), h2u(k[2], k[3]), h2u(k[4], k[5]), h2u(k[6], k[7]));
+            });
+        } else {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) *at(sK, c) = zero;
+        }
         const uint32_t there = __ballot_sync(kFull, page != nullptr);
         TileMeta *m = a.meta + item;
         if (hh == 0 && lane == 0) m->mask[warp] = there;
@@ -364,8 +438,8 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         }
         tc05::fence_proxy_async_smem();
         tc05::fence_before_sync();
-        __syncthreads();
-        if (tid == 0) {
+        timeout = __syncthreads_or(!ok);               // also: every thread has its part of the product
+        if (tid == 0 && !timeout) {
             bulk_s2g(a.images + size_t(item) * 2 * kImg, sK, 2 * kImg);   // keys, then values
             bulk_commit();
         }
@@ -391,6 +465,7 @@ struct AttendArgs {
     const int32_t *cu_q, *kv_lens;
     int total_q, max_q, max_kv_len;
     int pair0, n_tiles;
+    const int32_t *order;
     const uint8_t *images;
     const TileMeta *meta;
     const float *ksigns, *vsigns;
@@ -443,7 +518,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     constexpr uint32_t kImg = uint32_t(image_bytes(D));
     constexpr int NS = ring_slots<D>();
     constexpr uint32_t TO = 256;                          // TMEM columns: S / P of the tiles at 0 and 128, O behind
-    const int pl = blockIdx.y, pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H, split = blockIdx.z;
+    const int pl = a.order[blockIdx.y], pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H, split = blockIdx.z;
     int q0;
     bool cut;
     const int nq = run_of(a, b, &q0, &cut);
@@ -678,7 +753,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             }
             finite = bad == 0.f;                           // a coordinate that is not finite spreads over the row
             int e;
-            const float down = tile_scale(finite ? mx : 0.f, &e);
+            const float down = scale_to(finite ? mx : 0.f, 11, &e);
             // log2(e) / sqrt(d) of the logit, 1 / sqrt(d) of the rotation
             rowc = ldexpf(1.4426950408889634f / float(D), e);
             uint8_t *dst = sQ + uint32_t(tt) * kImg;
@@ -857,7 +932,7 @@ constexpr size_t kImageBudget = size_t(1) << 30;
 
 struct TcPlan {
     int n_tiles, pairs, round, x, n_splits, split_tiles;
-    size_t off_meta, off_img, off_po, off_pml, total;
+    size_t off_order, off_meta, off_img, off_po, off_pml, total;
 };
 
 TcPlan tc_plan(const Layout &L, const CrossShape &s) {
@@ -881,6 +956,7 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     p.n_splits = (p.n_tiles + p.split_tiles - 1) / p.split_tiles;
     size_t off = kWsHeader;
     auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) & ~size_t(255); return o; };
+    p.off_order = take(size_t(p.round) * 4);
     p.off_meta = take(size_t(p.round) * p.n_tiles * sizeof(TileMeta));
     p.off_img = take(size_t(p.round) * pair_bytes);
     const size_t rows = size_t(s.total_q) * s.Hq * p.n_splits;
@@ -911,6 +987,8 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
     x.cache = cache;
     x.num_blocks = num_blocks;
     x.n_tiles = p.n_tiles;
+    x.order = reinterpret_cast<int32_t *>(ws + p.off_order);
+    x.B = s.B;
     x.images = ws + p.off_img;
     x.meta = reinterpret_cast<TileMeta *>(ws + p.off_meta);
     x.status = reinterpret_cast<uint32_t *>(ws);
@@ -926,6 +1004,7 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
     a.max_q = s.max_q;
     a.max_kv_len = s.max_kv_len;
     a.n_tiles = p.n_tiles;
+    a.order = x.order;
     a.images = x.images;
     a.meta = x.meta;
     a.ksigns = kp->dev.signs;
