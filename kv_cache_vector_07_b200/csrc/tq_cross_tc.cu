@@ -138,63 +138,85 @@ struct HalfCode {
     const float *lv;                       // levels by code (shared memory)
 };
 
-// coord(i, y) for the thread's D / 2 coordinates, without their norm.
-template <int D, int W, bool SIGNS, typename F>
-__device__ __forceinline__ void walk_codes(const HalfCode &hc, const uint8_t *page, int pos, F &&chunk) {
-    constexpr int HALF = D / 2, BYTES = HALF * W / 8, WORDS = BYTES < 4 ? 1 : BYTES / 4;
-    uint32_t w[WORDS], sg[HALF / 32];
+// The bytes of the thread's D / 2 codes of up to 4 bits, as they lie in the
+// page, and a 3-bit code's sign bits.
+template <int D>
+struct HalfBytes {
+    uint32_t w[D / 16], sg[D / 64];
+};
+template <int D>
+__device__ __forceinline__ void fetch_codes(const HalfCode &hc, const uint8_t *page, int pos, HalfBytes<D> &v) {
     const uint8_t *at = page + hc.off + pos * hc.bpt;
-    if constexpr (BYTES >= 16) {
+    auto vec = [&](int i) {                            // 16 bytes
+        const uint4 u = reinterpret_cast<const uint4 *>(at)[i];
+        v.w[4 * i] = u.x; v.w[4 * i + 1] = u.y; v.w[4 * i + 2] = u.z; v.w[4 * i + 3] = u.w;
+    };
+    if (hc.width == 4) {
 #pragma unroll
-        for (int i = 0; i < BYTES / 16; ++i) {
-            const uint4 v = reinterpret_cast<const uint4 *>(at)[i];
-            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        for (int i = 0; i < D / 64; ++i) vec(i);
+    } else if (hc.width == 2) {
+        if constexpr (D == 128) {
+            vec(0);
+        } else {
+            v.w[0] = reinterpret_cast<const uint32_t *>(at)[0];
+            v.w[1] = reinterpret_cast<const uint32_t *>(at)[1];
         }
-    } else {
+    } else if (hc.width == 1) {
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(at)[i];
+        for (int i = 0; i < D / 64; ++i) v.w[i] = reinterpret_cast<const uint32_t *>(at)[i];
     }
+    if (hc.signs) {
 #pragma unroll
-    for (int i = 0; i < HALF / 32; ++i)
-        sg[i] = SIGNS ? reinterpret_cast<const uint32_t *>(page + hc.hoff + pos * hc.hbpt)[i] : 0u;
+        for (int i = 0; i < D / 64; ++i) v.sg[i] = reinterpret_cast<const uint32_t *>(page + hc.hoff + pos * hc.hbpt)[i];
+    }
+}
+
+// chunk(c, y) for the thread's coordinates, eight at a time, without their norm.
+template <int D, int W, bool SIGNS, typename F>
+__device__ __forceinline__ void walk_codes(const HalfCode &hc, const HalfBytes<D> &v, F &&chunk) {
 #pragma unroll
-    for (int c = 0; c < HALF / 8; ++c) {
+    for (int c = 0; c < D / 16; ++c) {
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = c * 8 + e;
-            if constexpr (W == 8) {
-                y[e] = e4m3_to_float(uint8_t(w[i >> 2] >> (8 * (i & 3))));
-            } else {
-                uint32_t k = (w[i * W / 32] >> (i * W % 32)) & ((1u << W) - 1u);
-                if (SIGNS) k |= ((sg[i >> 5] >> (i & 31)) & 1u) << 2;
-                y[e] = hc.lv[k];
-            }
+            uint32_t k = (v.w[i * W / 32] >> (i * W % 32)) & ((1u << W) - 1u);
+            if (SIGNS) k |= ((v.sg[i >> 5] >> (i & 31)) & 1u) << 2;
+            y[e] = hc.lv[k];
         }
         chunk(c, y);
     }
 }
 template <int D, typename F>
-__device__ __forceinline__ void walk(const HalfCode &hc, const uint8_t *page, int pos, int hh, int off2, int bpt2,
-                                     const float *polar, F &&chunk) {
+__device__ __forceinline__ void walk(const HalfCode &hc, const HalfBytes<D> &v, const uint8_t *page, int pos, int hh,
+                                     int off2, int bpt2, const float *polar, F &&chunk) {
     switch (hc.width) {
-        case 4: walk_codes<D, 4, false>(hc, page, pos, chunk); break;
+        case 4: walk_codes<D, 4, false>(hc, v, chunk); break;
         case 2:
-            if (hc.signs) walk_codes<D, 2, true>(hc, page, pos, chunk);
-            else walk_codes<D, 2, false>(hc, page, pos, chunk);
+            if (hc.signs) walk_codes<D, 2, true>(hc, v, chunk);
+            else walk_codes<D, 2, false>(hc, v, chunk);
             break;
-        case 1: walk_codes<D, 1, false>(hc, page, pos, chunk); break;
-        case 8: walk_codes<D, 8, false>(hc, page, pos, chunk); break;
+        case 1: walk_codes<D, 1, false>(hc, v, chunk); break;
+        case 8:                                        // E4M3 bytes, read here
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const uint2 u = reinterpret_cast<const uint2 *>(page + hc.off + pos * hc.bpt)[c];
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = e4m3_to_float(uint8_t((e < 4 ? u.x : u.y) >> (8 * (e & 3))));
+                chunk(c, y);
+            }
+            break;
         default:
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
                 float y[8];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const float2 v = polar_pair<D>(page + hc.off + pos * hc.bpt, page + off2 + pos * bpt2, polar,
+                    const float2 u = polar_pair<D>(page + hc.off + pos * hc.bpt, page + off2 + pos * bpt2, polar,
                                                    hh * (D / 4) + 4 * c + p);
-                    y[2 * p] = v.x;
-                    y[2 * p + 1] = v.y;
+                    y[2 * p] = u.x;
+                    y[2 * p + 1] = u.y;
                 }
                 chunk(c, y);
             }
@@ -285,12 +307,11 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
-    if (tid < 2) {
-        float mx = 0.f;
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(lv[2 * tid + (i >> 4)][i & 15]));
-        if (tid == 0 && L.kbits == 8) mx = 448.f * rsqrtf(float(D));
-        if (tid == 0 ? L.kpolar : L.vpolar) mx = 1.f;
-        bound[tid] = mx;
+    if (warp < 2) {
+        float mx = warp_max(fabsf(lv[2 * warp + (lane >> 4)][lane & 15]));
+        if (warp == 0 && L.kbits == 8) mx = 448.f * rsqrtf(float(D));
+        if (warp == 0 ? L.kpolar : L.vpolar) mx = 1.f;
+        if (lane == 0) bound[warp] = mx;
     }
     __syncthreads();
     const uint32_t tmem = tmem_holder, lrow = uint32_t((warp & 3) * 32) << 16;
@@ -314,26 +335,94 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     uint32_t phase = 0;
     bool timeout = false;
 
-    const int64_t items = int64_t(a.n_pairs) * a.n_tiles;
-    for (int64_t item = blockIdx.x; item < items && !timeout; item += gridDim.x) {
-        const int pl = int(item / a.n_tiles), tile = int(item - int64_t(pl) * a.n_tiles);
-        const int pair = a.pair0 + pl, b = pair / L.H, h = pair - b * L.H;
-        const int len = min(max(a.kv_lens[b], 0), a.max_kv_len);
-        if (tile * kTile >= len) continue;
-        const int t = tile * kTile + key, pos = t % L.P;
-        const uint8_t *page = nullptr;
-        float nk = 0.f, nv = 0.f, rk = 0.f;
+    // Three items are on their way at once: where this thread's key of an item
+    // lies is looked up two items ahead, its norms, signs and codes are loaded
+    // one ahead (one round of loads after another took 8,000 of an item's
+    // 15,000 cycles)
+    struct Place {
+        int there;                                     // 0: no such item, 1: key absent, 2: present
+        int pos;
+        const uint8_t *page;
+        unsigned image;                                // the tile's place in images and meta
+    };
+    struct Raw {
+        Place at;
+        uint16_t nk, nv, rk;
+        uint32_t sign[D / 64];
+        HalfBytes<D> k, v;
+    };
+    // Items are the tiles that there are, sequence after sequence: seq holds the
+    // one that the last item asked for lies in, before_seq the items before it
+    // (stepping over the empty tiles of short sequences one by one cost as much
+    // as a third of the tiles that hold something).
+    const int last = a.pair0 + a.n_pairs;
+    int seq = a.pair0 / L.H, seq_tiles = 0, seq_first = a.pair0;
+    unsigned before_seq = 0, seq_items = 0;
+    auto enter = [&](int b) {                          // sequence b and its pairs in this launch
+        seq = b;
+        seq_first = max(a.pair0, b * L.H);
+        const int pairs = min(last, (b + 1) * L.H) - seq_first;
+        if (pairs <= 0) return false;
+        seq_tiles = (min(max(a.kv_lens[b], 0), a.max_kv_len) + kTile - 1) / kTile;
+        seq_items = unsigned(pairs) * unsigned(seq_tiles);
+        return true;
+    };
+    bool more = enter(seq);
+    auto place = [&](unsigned item) {
+        Place p{0, 0, nullptr, 0u};
+        while (more && item - before_seq >= seq_items) {
+            before_seq += seq_items;
+            more = enter(seq + 1);
+        }
+        if (!more) return p;
+        const int within = int(item - before_seq), q = within / seq_tiles, tile = within - q * seq_tiles;
+        const int pair = seq_first + q;
+        const int len = min(max(a.kv_lens[seq], 0), a.max_kv_len);
+        const int t = tile * kTile + key, pg = t / L.P;
+        p.there = 1;
+        p.pos = t - pg * L.P;
+        p.image = unsigned(pair - a.pair0) * unsigned(a.n_tiles) + unsigned(tile);
         if (t < len) {
-            const int blk = a.table[int64_t(b) * a.bt_stride + t / L.P];
+            const int blk = a.table[int64_t(seq) * a.bt_stride + pg];
             if (blk >= 0 && blk < a.num_blocks) {
-                page = a.cache + (int64_t(blk) * L.H + h) * int64_t(L.page_bytes);
-                nk = h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kn_off + pos * 2));
-                nv = h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.vn_off + pos * 2));
-                if (L.kqjl) rk = cq * h2f_bits(*reinterpret_cast<const uint16_t *>(page + L.kr_off + pos * 2));
+                p.there = 2;
+                p.page = a.cache + (int64_t(blk) * L.H + (pair - seq * L.H)) * int64_t(L.page_bytes);
             } else {
                 atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
             }
         }
+        return p;
+    };
+    auto fetch = [&](const Place &at) {
+        Raw r;
+        r.at = at;
+        r.nk = r.nv = r.rk = 0;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) r.sign[i] = 0u;
+        if (at.there == 2) {
+            r.nk = *reinterpret_cast<const uint16_t *>(at.page + L.kn_off + at.pos * 2);
+            r.nv = *reinterpret_cast<const uint16_t *>(at.page + L.vn_off + at.pos * 2);
+            if (L.kqjl) {
+                r.rk = *reinterpret_cast<const uint16_t *>(at.page + L.kr_off + at.pos * 2);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    r.sign[i] =
+                        reinterpret_cast<const uint32_t *>(at.page + L.ks_off + at.pos * L.ks_bpt + hh * (HALF / 8))[i];
+            }
+            fetch_codes<D>(kc, at.page, at.pos, r.k);
+            fetch_codes<D>(vc, at.page, at.pos, r.v);
+        }
+        return r;
+    };
+    Raw coming = fetch(place(blockIdx.x));
+    Place ahead = place(blockIdx.x + gridDim.x);
+    for (unsigned item = blockIdx.x; coming.at.there && !timeout; item += gridDim.x) {
+        const Raw raw = coming;
+        coming = fetch(ahead);
+        ahead = place(item + 2 * gridDim.x);
+        const int pos = raw.at.pos;
+        const uint8_t *page = raw.at.page;
+        const float nk = h2f_bits(raw.nk), nv = h2f_bits(raw.nv), rk = cq * h2f_bits(raw.rk);
         if (tid == 0) bulk_wait_read();                // the tiles of the item before have been read
         // a key's coordinate is below bound nk + rk sum_j |S_ji|, and |S_ji| below
         // 8.6 (Box-Muller of 53-bit uniforms)
@@ -358,8 +447,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         if (L.kqjl) {
 #pragma unroll
             for (int c = 0; c < NC; c += 4) {
-                const uint32_t bits =
-                    page ? *reinterpret_cast<const uint32_t *>(page + L.ks_off + pos * L.ks_bpt + hh * (HALF / 8) + c) : 0u;
+                const uint32_t bits = raw.sign[c / 4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w[4];
@@ -390,7 +478,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         if (page) {
             const float f = nv * vsc;
-            walk<D>(vc, page, pos, hh, L.vc2_off, L.vc2_bpt, polar[1], [&](int c, const float (&y)[8]) {
+            walk<D>(vc, raw.v, page, pos, hh, L.vc2_off, L.vc2_bpt, polar[1], [&](int c, const float (&y)[8]) {
                 *at(sV, c) = make_uint4(h2u(y[0] * f, y[1] * f), h2u(y[2] * f, y[3] * f), h2u(y[4] * f, y[5] * f),
                                         h2u(y[6] * f, y[7] * f));
             });
@@ -404,7 +492,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
             tc05::fence_after_sync();
         }
         ++phase;
-        // keys: the thread's part of the product comes 32 coordinates at a time
+        // keys
         uint32_t r[HALF];
         if (L.kqjl) {
 #pragma unroll
@@ -417,7 +505,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         }
         if (page) {
             const float f = nk * ksc * (L.kbits == 8 ? rsqrtf(float(D)) : 1.f), g = rk * ksc;
-            walk<D>(kc, page, pos, hh, L.kc2_off, L.kc2_bpt, polar[0], [&](int c, const float (&y)[8]) {
+            walk<D>(kc, raw.k, page, pos, hh, L.kc2_off, L.kc2_bpt, polar[0], [&](int c, const float (&y)[8]) {
                 float k[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) k[e] = fmaf(g, __uint_as_float(r[c * 8 + e]), y[e] * f);
@@ -428,7 +516,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
             for (int c = 0; c < NC; ++c) *at(sK, c) = zero;
         }
         const uint32_t there = __ballot_sync(kFull, page != nullptr);
-        TileMeta *m = a.meta + item;
+        TileMeta *m = a.meta + raw.at.image;
         if (hh == 0 && lane == 0) m->mask[warp] = there;
         if (tid == 0) {
             m->kscale = ldexpf(1.f, ek);
@@ -440,7 +528,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         tc05::fence_before_sync();
         timeout = __syncthreads_or(!ok);               // also: every thread has its part of the product
         if (tid == 0 && !timeout) {
-            bulk_s2g(a.images + size_t(item) * 2 * kImg, sK, 2 * kImg);   // keys, then values
+            bulk_s2g(a.images + size_t(raw.at.image) * 2 * kImg, sK, 2 * kImg);   // keys, then values
             bulk_commit();
         }
     }
