@@ -183,27 +183,33 @@ def _dev_check(*tensors):
             raise ValueError("libtqkv arguments must be contiguous CUDA tensors")
 
 
-def _same_device(*tensors) -> int:
+def _one_device(*tensors) -> int:
     """The index of the one CUDA device that all given tensors are on."""
-    at = {t.device for t in tensors if t is not None}
-    if len(at) != 1 or next(iter(at)).type != "cuda":
-        raise ValueError("libtqkv arguments must be CUDA tensors of one device")
-    return next(iter(at)).index
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            at = t.get_device()
+            if at < 0 or (dev >= 0 and at != dev):
+                raise ValueError("libtqkv arguments must be CUDA tensors of one device")
+            dev = at
+    return dev
 
 
-class _on:
-    """The given device made current for a call, where it is not already."""
-
-    def __init__(self, index: int):
-        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _call(dev: int, name: str, stream, *args):
+    """The C entry point `name` with args and a stream of device dev, which is
+    made current for the call where it is not already."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    f = getattr(_lib, name)
+    if dev == torch.cuda.current_device():
+        code = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, stream)
+    if code != TQ_OK:
+        raise TQError(code, name)
 
 
 # ---------------------------------------------------------------------------
@@ -283,6 +289,10 @@ def cache_bytes(desc: CacheDesc) -> int:
     out = _sz()
     _check(_lib.tq_cache_bytes(ctypes.byref(desc), ctypes.byref(out)), "tq_cache_bytes")
     return int(out.value)
+
+
+def _is_cache(c: torch.Tensor, num_blocks: int, heads: int, page: int) -> bool:
+    return c.dtype is torch.uint8 and c.is_contiguous() and c.shape == (num_blocks, heads, page)
 
 
 def alloc_cache(desc: CacheDesc, num_blocks: int, device="cuda") -> torch.Tensor:
@@ -448,31 +458,30 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
     Hq, d] see all kv_lens[b] tokens of sequence b (block_table [B, max_blocks]).
     Rows of out that belong to no run are not written (zero where out is not
     given).  lse fp32 [total_q, Hq], optional."""
+    dev = _one_device(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
     _dev_check(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
-    dev = _same_device(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
-    if Q.dim() != 3 or Q.shape[2] != desc.d or Q.dtype != torch.bfloat16:
+    if Q.dim() != 3 or Q.dtype is not torch.bfloat16 or Q.size(2) != desc.d:
         raise ValueError("Q must be bf16 [total_q, Hq, d]")
-    B = kv_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or kv_lens.shape != (B,) or cu_q.shape != (B + 1,):
-        raise ValueError("block_table must be [B, max_blocks], kv_lens [B] and cu_q [B + 1]")
-    if any(t.dtype != torch.int32 for t in (cu_q, block_table, kv_lens)):
-        raise ValueError("cu_q, block_table and kv_lens must be int32")
-    if cache.dtype != torch.uint8 or cache.shape[1:] != (desc.n_kv_heads, cache_bytes(desc)):
-        raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
-    if out is not None and (out.shape != Q.shape or out.dtype != Q.dtype):
-        raise ValueError("out must have Q's shape and dtype")
     total_q, Hq, _ = Q.shape
-    if lse is not None and (lse.shape != (total_q, Hq) or lse.dtype != torch.float32):
+    B = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.size(0) != B or kv_lens.dim() != 1 or cu_q.dim() != 1 or \
+            cu_q.numel() != B + 1:
+        raise ValueError("block_table must be [B, max_blocks], kv_lens [B] and cu_q [B + 1]")
+    if not (cu_q.dtype is block_table.dtype is kv_lens.dtype is torch.int32):
+        raise ValueError("cu_q, block_table and kv_lens must be int32")
+    if cache.dim() != 3 or not _is_cache(cache, cache.size(0), desc.n_kv_heads, cache_bytes(desc)):
+        raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
+    if out is None:
+        out = torch.zeros_like(Q)
+    elif out.shape != Q.shape or out.dtype is not Q.dtype:
+        raise ValueError("out must have Q's shape and dtype")
+    if lse is not None and (lse.shape != (total_q, Hq) or lse.dtype is not torch.float32):
         raise ValueError("lse must be fp32 [total_q, Hq]")
-    with _on(dev):
-        if out is None:
-            out = torch.zeros_like(Q)
-        if workspace is None:
-            workspace = _workspace(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), Q.device)
-        _check(_lib.tq_cross_attn(kp.handle, vp.handle, ctypes.byref(desc), _ptr(Q), total_q, max_q, Hq, _ptr(cu_q), B,
-                                  _ptr(block_table), block_table.shape[1], _ptr(kv_lens), max_kv_len, _ptr(cache),
-                                  cache.shape[0], _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "tq_cross_attn")
+    if workspace is None:
+        workspace = _workspace(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), Q.device)
+    _call(dev, "tq_cross_attn", stream, kp.handle, vp.handle, ctypes.byref(desc), Q.data_ptr(), total_q, max_q, Hq,
+          cu_q.data_ptr(), B, block_table.data_ptr(), block_table.size(1), kv_lens.data_ptr(), max_kv_len,
+          cache.data_ptr(), cache.size(0), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -483,25 +492,31 @@ def pages_workspace_bytes(num_blocks: int, n_rows: int, max_blocks: int) -> int:
     return int(_lib.tq_pages_workspace_bytes(num_blocks, n_rows, max_blocks))
 
 
-def _pool(desc, refs, table, lens, caches, ints, workspace):
-    """(device index, tq_page_pool, cache pointers, workspace) of a pages call."""
-    layers = () if caches is None else [caches] if isinstance(caches, torch.Tensor) else list(caches)
-    dev = _same_device(refs, table, lens, workspace, *ints, *layers)
-    if refs.dim() != 1 or table.dim() != 2 or lens.shape != table.shape[:1]:
-        raise ValueError("refs must be [num_blocks], table [n_rows, max_blocks] and lens [n_rows]")
+def _pool(desc, refs, table, lens, ints, workspace, caches=None):
+    """(device index, tq_page_pool, workspace, cache pointers) of a pages call."""
+    dev = _one_device(refs, table, lens, workspace, *ints)
     for t in (refs, table, lens, *ints):
-        if t.dtype != torch.int32 or not t.is_contiguous():
+        if t.dtype is not torch.int32 or not t.is_contiguous():
             raise ValueError("refs, table, lens and the requests must be contiguous int32 tensors")
-    if caches is not None and not layers:
-        raise ValueError("caches must name one cache at least")
-    for c in layers:
-        if c.dtype != torch.uint8 or not c.is_contiguous() or \
-                c.shape != (refs.shape[0], desc.n_kv_heads, cache_bytes(desc)):
-            raise ValueError("every cache must be contiguous uint8 [num_blocks, n_kv_heads, page bytes]")
+    if refs.dim() != 1 or table.dim() != 2 or lens.dim() != 1 or lens.numel() != table.size(0):
+        raise ValueError("refs must be [num_blocks], table [n_rows, max_blocks] and lens [n_rows]")
+    num_blocks, (n_rows, max_blocks) = refs.numel(), table.shape
+    ptrs = None
+    if caches is not None:
+        layers = [caches] if isinstance(caches, torch.Tensor) else caches
+        page = cache_bytes(desc)
+        ptrs = (_vp * len(layers))()
+        for i, c in enumerate(layers):
+            if c.get_device() != dev or not _is_cache(c, num_blocks, desc.n_kv_heads, page):
+                raise ValueError("every cache must be contiguous uint8 [num_blocks, n_kv_heads, page bytes] on the "
+                                 "tables' device")
+            ptrs[i] = c.data_ptr()
+        if not ptrs:
+            raise ValueError("caches must name one cache at least")
     if workspace is None:
-        workspace = _workspace(pages_workspace_bytes(refs.shape[0], *table.shape), refs.device)
-    pool = _PagePool(refs.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.shape[0], *table.shape)
-    return dev, pool, (_vp * len(layers))(*[c.data_ptr() for c in layers]), workspace
+        workspace = _workspace(pages_workspace_bytes(num_blocks, n_rows, max_blocks), refs.device)
+    pool = _PagePool(refs.data_ptr(), table.data_ptr(), lens.data_ptr(), num_blocks, n_rows, max_blocks)
+    return dev, pool, workspace, ptrs
 
 
 def pages_reserve(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -511,13 +526,11 @@ def pages_reserve(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens
     tokens of every row; slot_mapping int32 [n_slots] receives their slots, row
     after row.  refs int32 [num_blocks], table int32 [n_rows, max_blocks] and
     lens int32 [n_rows] are updated.  Returns the workspace (read_status)."""
-    dev, pool, _, workspace = _pool(desc, refs, table, lens, None, (new_tokens, slot_mapping), workspace)
+    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (new_tokens, slot_mapping), workspace)
     if new_tokens.shape != lens.shape or slot_mapping.dim() != 1:
         raise ValueError("new_tokens must be [n_rows] and slot_mapping [n_slots]")
-    with _on(dev):
-        _check(_lib.tq_pages_reserve(ctypes.byref(desc), ctypes.byref(pool), _ptr(new_tokens), _ptr(slot_mapping),
-                                     slot_mapping.numel(), _ptr(workspace), workspace.numel(), _stream(stream)),
-               "tq_pages_reserve")
+    _call(dev, "tq_pages_reserve", stream, ctypes.byref(desc), ctypes.byref(pool), new_tokens.data_ptr(),
+          slot_mapping.data_ptr(), slot_mapping.numel(), workspace.data_ptr(), workspace.numel())
     return workspace
 
 
@@ -527,13 +540,11 @@ def pages_fork(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tensor,
     """tq_pages_fork: rows dst_rows (empty) become copies of rows src_rows
     (int32 [n]); caches: one cache, or a list with every layer's.  Full pages
     are shared, partly filled ones copied.  Returns the workspace."""
-    dev, pool, ptrs, workspace = _pool(desc, refs, table, lens, caches, (src_rows, dst_rows), workspace)
+    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (src_rows, dst_rows), workspace, caches)
     if src_rows.dim() != 1 or src_rows.shape != dst_rows.shape:
         raise ValueError("src_rows and dst_rows must be [n]")
-    with _on(dev):
-        _check(_lib.tq_pages_fork(ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), _ptr(src_rows),
-                                  _ptr(dst_rows), src_rows.numel(), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "tq_pages_fork")
+    _call(dev, "tq_pages_fork", stream, ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), src_rows.data_ptr(),
+          dst_rows.data_ptr(), src_rows.numel(), workspace.data_ptr(), workspace.numel())
     return workspace
 
 
@@ -543,13 +554,11 @@ def pages_compact(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tens
     """tq_pages_compact: row rows[i] keeps its tokens keep[i, :keep_lens[i]]
     (int32 [n], [n, most], [n]), in that order; caches as in pages_fork.
     Returns the workspace."""
-    dev, pool, ptrs, workspace = _pool(desc, refs, table, lens, caches, (rows, keep, keep_lens), workspace)
-    if rows.dim() != 1 or keep.dim() != 2 or keep.shape[0] != rows.shape[0] or keep_lens.shape != rows.shape:
+    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (rows, keep, keep_lens), workspace, caches)
+    if rows.dim() != 1 or keep.dim() != 2 or keep.size(0) != rows.numel() or keep_lens.shape != rows.shape:
         raise ValueError("rows and keep_lens must be [n] and keep [n, most]")
-    with _on(dev):
-        _check(_lib.tq_pages_compact(ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), _ptr(rows), _ptr(keep),
-                                     keep.shape[1], _ptr(keep_lens), rows.numel(), _ptr(workspace),
-                                     workspace.numel(), _stream(stream)), "tq_pages_compact")
+    _call(dev, "tq_pages_compact", stream, ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), rows.data_ptr(),
+          keep.data_ptr(), keep.size(1), keep_lens.data_ptr(), rows.numel(), workspace.data_ptr(), workspace.numel())
     return workspace
 
 
@@ -557,12 +566,11 @@ def pages_free(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens: t
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """tq_pages_free: rows (int32 [n]) give their pages back and become empty.
     Returns the workspace."""
-    dev, pool, _, workspace = _pool(desc, refs, table, lens, None, (rows,), workspace)
+    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (rows,), workspace)
     if rows.dim() != 1:
         raise ValueError("rows must be [n]")
-    with _on(dev):
-        _check(_lib.tq_pages_free(ctypes.byref(desc), ctypes.byref(pool), _ptr(rows), rows.numel(), _ptr(workspace),
-                                  workspace.numel(), _stream(stream)), "tq_pages_free")
+    _call(dev, "tq_pages_free", stream, ctypes.byref(desc), ctypes.byref(pool), rows.data_ptr(), rows.numel(),
+          workspace.data_ptr(), workspace.numel())
     return workspace
 
 
@@ -584,17 +592,20 @@ _ROPE_DTYPES = {torch.bfloat16: TQ_DTYPE_BF16, torch.float32: TQ_DTYPE_F32}
 
 
 def _heads(x, weight, out, d, n, name):
+    """(tq_heads, result tensor) of one side of qk_norm_rope."""
     if x is None:
         return None, None
+    if x.dim() != 3 or x.size(0) != n or x.size(2) != d:
+        raise ValueError(f"{name} must be [n_tokens, heads, d]")
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    for t, what in ((x, name), (out, name + "_out")):
-        if t.dim() != 3 or t.shape[2] != d or t.shape[0] != n or (d > 1 and t.stride(2) != 1):
-            raise ValueError(f"{what} must be [n_tokens, heads, d] with adjacent coordinates")
-    if out.shape != x.shape or out.dtype != x.dtype:
+    elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError(f"{name}_out must have {name}'s shape and dtype")
-    return _Heads(x.data_ptr(), x.stride(0), x.stride(1), _ptr(weight), out.data_ptr(), out.stride(0), out.stride(1),
-                  x.shape[1]), out
+    (xt, xh, xd), (ot, oh, od) = x.stride(), out.stride()
+    if xd != 1 or od != 1:
+        raise ValueError(f"the coordinates of {name} and {name}_out must be adjacent")
+    return _Heads(x.data_ptr(), xt, xh, None if weight is None else weight.data_ptr(), out.data_ptr(), ot, oh,
+                  x.size(1)), out
 
 
 def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
@@ -607,30 +618,32 @@ def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None,
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    n = x.shape[0]
-    dev = _same_device(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    n = x.size(0)
+    dev = _one_device(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     dt = _ROPE_DTYPES.get(x.dtype)
-    if dt is None or (q is not None and k is not None and q.dtype != k.dtype):
+    if dt is None or (k is not None and k.dtype is not x.dtype):
         raise ValueError("q and k must both be bf16 or both fp32")
-    weights = [w for w in (q_weight, k_weight) if w is not None]
-    if any(w.shape != (desc.d,) or not w.is_contiguous() or w.dtype not in _ROPE_DTYPES or w.dtype != weights[0].dtype
-           for w in weights):
-        raise ValueError("weights must be contiguous [d], both bf16 or both fp32")
-    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float32:
+    wt = dt
+    for w in (q_weight, k_weight):
+        if w is not None:
+            wt = _ROPE_DTYPES.get(w.dtype)
+            if wt is None or w.dim() != 1 or w.numel() != desc.d or not w.is_contiguous():
+                raise ValueError("weights must be contiguous [d], bf16 or fp32")
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise ValueError("the weights must both be bf16 or both fp32")
+    if positions.dtype is not torch.int32 or inv_freq.dtype is not torch.float32:
         raise ValueError("positions must be int32 and inv_freq fp32")
-    if positions.shape not in ((n,), (desc.n_axes, n)) or (positions.dim() == 1 and desc.n_axes != 1) or \
+    axes = positions.dim()
+    if axes not in (1, 2) or positions.size(-1) != n or (positions.size(0) if axes == 2 else 1) != desc.n_axes or \
             (n > 1 and positions.stride(-1) != 1):
         raise ValueError("positions must be [n_tokens], or [n_axes, n_tokens], with adjacent tokens")
     if inv_freq.numel() != desc.rot_dim // 2 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous [rot_dim / 2]")
     hq, q_out = _heads(q, q_weight, q_out, desc.d, n, "q")
     hk, k_out = _heads(k, k_weight, k_out, desc.d, n, "k")
-    axis_stride = positions.stride(0) if positions.dim() == 2 else n
-    with _on(dev):
-        _check(_lib.tq_qk_norm_rope(ctypes.byref(desc), dt, _ROPE_DTYPES[weights[0].dtype] if weights else dt, n,
-                                    ctypes.byref(hq) if hq is not None else None,
-                                    ctypes.byref(hk) if hk is not None else None, _ptr(positions), axis_stride,
-                                    _ptr(inv_freq), _stream(stream)), "tq_qk_norm_rope")
+    _call(dev, "tq_qk_norm_rope", stream, ctypes.byref(desc), dt, wt, n, None if hq is None else ctypes.byref(hq),
+          None if hk is None else ctypes.byref(hk), positions.data_ptr(), positions.stride(0) if axes == 2 else n,
+          inv_freq.data_ptr())
     return q_out, k_out
 
 
