@@ -716,7 +716,7 @@ int run_attention(const tq_params *kp, const tq_params *vp, const Layout &L, con
     c.vp = vp->dev;
     c.out = out;
     c.lse = lse;
-    c.row_lens = s.skip_negative ? s.seq_lens : nullptr;
+    c.row_lens = s.cross ? s.seq_lens : nullptr;
     c.Q = static_cast<const __nv_bfloat16 *>(Q);
     const int64_t crow = int64_t(p.n_groups) * p.G;
     combine_kernel<D><<<unsigned((crow + 3) / 4), 128, 0, st>>>(c);

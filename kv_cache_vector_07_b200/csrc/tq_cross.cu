@@ -54,7 +54,7 @@ AttnShape rows_shape(const Layout &L, const CrossShape &s) {
     r.max_blocks = (s.max_kv_len + L.P - 1) / L.P;
     r.bt_stride = r.max_blocks;
     r.is_decode = 1;
-    r.skip_negative = 1;
+    r.cross = 1;
     r.max_len = s.max_kv_len;
     return r;
 }

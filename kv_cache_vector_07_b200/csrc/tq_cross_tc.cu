@@ -1035,10 +1035,12 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     if (fit > 65535) fit = 65535;
     p.round = int(fit < size_t(p.pairs) ? fit : size_t(p.pairs));
     p.x = (s.max_q + 2 * PT - 1) / (2 * PT);
-    // few blocks: the key axis is split, into pieces of at least four tiles
+    // fewer than three waves of blocks: the key axis is split, into pieces of at
+    // least eight tiles (8 runs of 77 x 32 heads over up to 4,096 states: 83 us
+    // unsplit, XX us with four pieces)
     const int64_t blocks = int64_t(p.x) * p.round;
-    int sp = int(148 / (blocks < 1 ? 1 : blocks));
-    if (sp > p.n_tiles / 4) sp = p.n_tiles / 4;
+    int sp = int((3 * 148 + blocks - 1) / (blocks < 1 ? 1 : blocks));
+    if (sp > p.n_tiles / 8) sp = p.n_tiles / 8;
     if (sp < 1) sp = 1;
     p.split_tiles = (p.n_tiles + sp - 1) / sp;
     p.n_splits = (p.n_tiles + p.split_tiles - 1) / p.split_tiles;

@@ -185,7 +185,7 @@ struct AttnShape {
     int base_len;         // prefill: seq_len - C (query j sees base_len + j + 1)
     int max_len;          // longest visible length
     int is_decode;        // 1: decode (per-sequence lengths), 0: prefill chunk
-    int skip_negative;    // 1: rows of a sequence with a negative length are not written
+    int cross;            // 1: rows of cross attention (those of a negative length are not written)
 };
 // New tokens of a fused decode step (one per sequence): bf16 K and V
 // [B][H][d], their slots, and the cache they are written into.
