@@ -277,12 +277,17 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
 
     if (blockIdx.x == 0) order_pairs(a);
     // S as the B operand: row j holds S[j][0 .. D), 64 columns to a half
-    if (L.kqjl)
-        for (int i = tid; i < D * D / 8; i += 256) {
-            const int j = i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<uint4 *>(sS + (c >> 3) * (D * 128) + tc05::sw128_offset(uint32_t(j), uint32_t(c & 7))) =
-                *reinterpret_cast<const uint4 *>(a.kp.S16 + size_t(j) * D + c * 8);
+    if (L.kqjl) {
+        constexpr int PER = D * D / 8 / 256;              // pieces of a thread, all asked for at once
+        uint4 v[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = reinterpret_cast<const uint4 *>(a.kp.S16)[k * 256 + tid];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = k * 256 + tid, j = i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4 *>(sS + (c >> 3) * (D * 128) + tc05::sw128_offset(uint32_t(j), uint32_t(c & 7))) = v[k];
         }
+    }
     // levels: keys' first and second codebook, values' first and second
     if (tid < 64) {
         const int i = tid & 15, which = tid >> 4;
@@ -990,21 +995,45 @@ __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant_
     if (i >= nq * a.G) return;
     const int64_t row = (int64_t(q0) + i / a.G) * a.Hq + h * a.G + i % a.G;
     const int64_t step = int64_t(a.total_q) * a.Hq;
+    // lane s holds split s of a round of 32: the weights of all are there before
+    // the first partial is asked for, and four partials are on their way at once
     float M = -INFINITY;
-    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, a.part_ml[(s * step + row) * 2]);
+    for (int s = lane; s < a.n_splits; s += 32)
+        if (a.part_ml[(s * step + row) * 2 + 1] != 0.f) M = fmaxf(M, a.part_ml[(s * step + row) * 2]);
+    M = warp_max(M);
     float l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int s = 0; s < a.n_splits; ++s) {
-        const float ls = a.part_ml[(s * step + row) * 2 + 1];
-        if (ls == 0.f) continue;                          // no key there
-        const float f = exp2f(a.part_ml[(s * step + row) * 2] - M);
-        l = fmaf(ls, f, l);
-        float v[E];
-        load_vec<D>(a.part_o + (s * step + row) * D, lane, v);
+    for (int s0 = 0; s0 < a.n_splits; s0 += 32) {
+        const int s = s0 + lane, n = min(32, a.n_splits - s0);
+        float f = 0.f;                                    // 0: no key there
+        if (s < a.n_splits) {
+            const float ls = a.part_ml[(s * step + row) * 2 + 1];
+            if (ls != 0.f) {
+                f = exp2f(a.part_ml[(s * step + row) * 2] - M);
+                l = fmaf(ls, f, l);
+            }
+        }
+        for (int i = 0; i < n; i += 4) {
+            float v[4][E], w[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], f, o[e]);
+            for (int k = 0; k < 4; ++k) {
+                w[k] = __shfl_sync(kFull, f, (i + k) & 31);
+                if (i + k >= n) w[k] = 0.f;
+                if (w[k] != 0.f) {
+                    load_vec<D>(a.part_o + ((s0 + i + k) * step + row) * D, lane, v[k]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(v[k][e], w[k], o[e]);
+        }
     }
+    l = warp_sum(l);
     fwht_warp<D>(o, lane);
     float sg[E];
     load_vec<D>(a.vsigns, lane, sg);
@@ -1037,7 +1066,7 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     p.x = (s.max_q + 2 * PT - 1) / (2 * PT);
     // fewer than three waves of blocks: the key axis is split, into pieces of at
     // least eight tiles (8 runs of 77 x 32 heads over up to 4,096 states: 83 us
-    // unsplit, XX us with four pieces)
+    // unsplit, 66 with four pieces and 7 to merge them)
     const int64_t blocks = int64_t(p.x) * p.round;
     int sp = int((3 * 148 + blocks - 1) / (blocks < 1 ? 1 : blocks));
     if (sp > p.n_tiles / 8) sp = p.n_tiles / 8;
