@@ -383,7 +383,7 @@ int tq_pages_reserve(const tq_cache_desc *desc, const tq_page_pool *pool, const 
 /* Row dst_rows[i] (empty) becomes a copy of row src_rows[i] (device arrays of
  * n <= n_rows): full pages are shared, a partly filled last page is copied
  * whole into a fresh page in each of the n_layers caches (host array of
- * device pointers).  A row may be forked many times; a dst row named twice is
+ * device pointers, 16-byte aligned).  A row may be forked many times; a dst row named twice is
  * served once, for the first. */
 int tq_pages_fork(const tq_cache_desc *desc, const tq_page_pool *pool, void *const *caches, int n_layers,
                   const int32_t *src_rows, const int32_t *dst_rows, int n, void *workspace, size_t workspace_bytes,

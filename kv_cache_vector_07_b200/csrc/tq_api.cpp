@@ -350,7 +350,7 @@ bool pool_ok(const tq_cache_desc *desc, const tq_page_pool *p, void *ws, size_t 
 bool layers_ok(void *const *caches, int n_layers) {
     if (!caches || n_layers < 1) return false;
     for (int i = 0; i < n_layers; ++i)
-        if (!caches[i] || !aligned(caches[i], 256)) return false;
+        if (!caches[i] || !aligned(caches[i], 16)) return false;   // layers of one tensor, say
     return true;
 }
 

@@ -608,6 +608,13 @@ Plan make_plan(const Layout &L, const AttnShape &s) {
             }
             if (waves >= 4.0) break;
         }
+        if (s.cross) {
+            // sequences of very different lengths: pieces of eight pages, up to
+            // two waves of them (32 rows over up to 2,048 tokens: 50 us in two
+            // pieces a row, 47 in four, 56 in eight)
+            const int64_t fill = p.n_groups > 0 ? 2 * slots / p.n_groups : 1;
+            best = max_sp < 1 || fill < 1 ? 1 : int(fill < max_sp ? fill : max_sp);
+        }
         split_len = (maxlen + best - 1) / best;
         split_len = (split_len + kChunk - 1) / kChunk * kChunk;
         splits = (maxlen + split_len - 1) / split_len;

@@ -23,6 +23,8 @@
 // ride along for nothing: the key's on the factor that turns S into a
 // logarithm, the value's (2^e) on its offset, P' = 2^(l + e - m) with m the
 // running maximum of l + e, while the sum takes P' 2^-e.
+#include <atomic>
+
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -1089,12 +1091,21 @@ template <int D>
 int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
            const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, cudaStream_t st) {
     const TcPlan p = tc_plan(L, s);
-    cudaError_t e = cudaFuncSetAttribute(cross_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(expand_smem<D>()));
+    // shared memory beyond the default is asked for once a device
+    static std::atomic<uint64_t> asked{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(cross_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(attend_smem<D>()));
-    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (!(asked.load(std::memory_order_acquire) & bit) || !bit) {
+        e = cudaFuncSetAttribute(cross_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(expand_smem<D>()));
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(cross_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(attend_smem<D>()));
+        if (e != cudaSuccess) return e;
+        asked.fetch_or(bit, std::memory_order_release);
+    }
     ExpandArgs x{};
     x.L = L;
     x.kp = kp->dev;
@@ -1151,9 +1162,16 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
 
 }  // namespace
 
+// Expanding the states pays once and for all rows, decoding by rows pays for
+// every one.  Where the tensor-core decode kernel serves the codec the two
+// meet at about five queries a run (8 x 32 heads over 2,048 states: 75 against
+// 80 us at four queries, 94 against 81 at six; 32 sequences: 195 against 244 at
+// four, 289 against 247 at six); where the general one would, expanding is
+// ahead from the first (8 x 1 query, d = 64: 191 against 46 us; FP8 keys in
+// pages of 16: 246 against 80).
 bool cross_tc_covers(const Layout &L, bool dense, const CrossShape &s) {
     if ((L.d != 64 && L.d != 128) || dense) return false;
-    return s.max_q > 4;
+    return s.max_q > 4 || dec128_resident(L, s.Hq / L.H) == 0;
 }
 
 size_t cross_tc_ws_bytes(const Layout &L, const CrossShape &s) { return tc_plan(L, s).total; }

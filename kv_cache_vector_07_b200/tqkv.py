@@ -11,6 +11,7 @@ not pass one; the library itself never allocates device memory outside
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -291,6 +292,16 @@ def cache_bytes(desc: CacheDesc) -> int:
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=256)
+def _page_bytes(*fields) -> int:
+    return cache_bytes(CacheDesc(*fields))
+
+
+def _page_of(desc: CacheDesc) -> int:
+    """cache_bytes, remembered by the description's values."""
+    return _page_bytes(desc.d, desc.kbits, desc.kqjl, desc.vbits, desc.page_tokens, desc.n_kv_heads)
+
+
 def _is_cache(c: torch.Tensor, num_blocks: int, heads: int, page: int) -> bool:
     return c.dtype is torch.uint8 and c.is_contiguous() and c.shape == (num_blocks, heads, page)
 
@@ -459,7 +470,9 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
     Rows of out that belong to no run are not written (zero where out is not
     given).  lse fp32 [total_q, Hq], optional."""
     dev = _one_device(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
-    _dev_check(Q, cu_q, block_table, kv_lens, cache, out, lse, workspace)
+    for t in (Q, cu_q, block_table, kv_lens, out, lse, workspace):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("libtqkv arguments must be contiguous CUDA tensors")
     if Q.dim() != 3 or Q.dtype is not torch.bfloat16 or Q.size(2) != desc.d:
         raise ValueError("Q must be bf16 [total_q, Hq, d]")
     total_q, Hq, _ = Q.shape
@@ -469,7 +482,7 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
         raise ValueError("block_table must be [B, max_blocks], kv_lens [B] and cu_q [B + 1]")
     if not (cu_q.dtype is block_table.dtype is kv_lens.dtype is torch.int32):
         raise ValueError("cu_q, block_table and kv_lens must be int32")
-    if cache.dim() != 3 or not _is_cache(cache, cache.size(0), desc.n_kv_heads, cache_bytes(desc)):
+    if cache.dim() != 3 or not _is_cache(cache, cache.size(0), desc.n_kv_heads, _page_of(desc)):
         raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
     if out is None:
         out = torch.zeros_like(Q)
@@ -504,7 +517,7 @@ def _pool(desc, refs, table, lens, ints, workspace, caches=None):
     ptrs = None
     if caches is not None:
         layers = [caches] if isinstance(caches, torch.Tensor) else caches
-        page = cache_bytes(desc)
+        page = _page_of(desc)
         ptrs = (_vp * len(layers))()
         for i, c in enumerate(layers):
             if c.get_device() != dev or not _is_cache(c, num_blocks, desc.n_kv_heads, page):

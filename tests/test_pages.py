@@ -352,6 +352,17 @@ def test_many_layers_and_no_requests():
 
 
 @pytest.mark.gpu
+def test_layers_that_are_slices_of_one_tensor():
+    """Their caches lie on 16 bytes, not on 256."""
+    p = Pair(d=64, kbits=2, vbits=4, P=16, H=1, num_blocks=13, n_rows=4, max_blocks=4, layers=3)
+    whole = torch.from_numpy(p.m.caches).to(DEV)
+    p.caches = list(whole.unbind(0))
+    assert any(c.data_ptr() % 256 for c in p.caches)
+    assert p.reserve([20, 5, 0, 0]) == 0 and p.fork([0, 1], [2, 3]) == 0
+    assert p.compact([2, 3], [[1, 19, 3], [4]]) == 0 and p.free([0, 1, 2, 3]) == 0
+
+
+@pytest.mark.gpu
 def test_large_pool_is_searched_to_its_end():
     n = 200000
     p = Pair(d=8, kbits=1, vbits=0, P=8, H=1, layers=1, num_blocks=n, n_rows=3, max_blocks=5000)
