@@ -284,6 +284,7 @@ bool cross_sizes_ok(const tq_cache_desc *desc, int B, int total_q, int max_q, in
     if (!valid_desc(desc) || desc->d > 256 || desc->vbits == 0) return false;
     if (B < 0 || total_q < 0 || max_q < 0 || max_kv_len < 0) return false;
     if (Hq < 1 || Hq % desc->n_kv_heads || Hq / desc->n_kv_heads > 8) return false;
+    if (total_q > INT32_MAX - 1024 || max_kv_len > INT32_MAX - 1024) return false;
     return int64_t(total_q) * Hq <= INT32_MAX && int64_t(B) * desc->n_kv_heads <= INT32_MAX;
 }
 

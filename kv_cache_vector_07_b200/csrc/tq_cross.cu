@@ -17,18 +17,18 @@ namespace {
 
 struct RowsArgs {
     const int32_t *cu_q, *table, *kv_lens;
-    int B, total_q, max_q, bt_stride, max_kv_len, P, width;
-    int32_t *row_len;        // [total_q], -1: the row belongs to no run
-    int32_t *row_table;      // [total_q][width]
+    int B, row0, n_rows, max_q, bt_stride, max_kv_len, P, width;
+    int32_t *row_len;        // [n_rows], -1: the row belongs to no run
+    int32_t *row_table;      // [n_rows][width]
     uint32_t *status;
 };
 
-// One warp per query row: its sequence (the last b with cu_q[b] <= row), that
+// One warp per query row of row0 .. row0 + n_rows - 1: its sequence (the last b with cu_q[b] <= row), that
 // sequence's length and its table row.
 __global__ void __launch_bounds__(128) cross_rows_kernel(RowsArgs a) {
     const int lane = threadIdx.x & 31;
-    const int row = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= a.total_q) return;
+    const int at = int(blockIdx.x) * 4 + (threadIdx.x >> 5), row = a.row0 + at;
+    if (at >= a.n_rows) return;
     int lo = 0, hi = a.B;                                  // cu_q[lo] <= row (or lo = 0), lo < hi
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -41,15 +41,23 @@ __global__ void __launch_bounds__(128) cross_rows_kernel(RowsArgs a) {
         if (row - begin < a.max_q) len = min(max(a.kv_lens[lo], 0), a.max_kv_len);
         else if (lane == 0) atomicOr(a.status, TQ_DEV_ROW);
     }
-    if (lane == 0) a.row_len[row] = len;
+    if (lane == 0) a.row_len[at] = len;
     const int pages = len > 0 ? (len + a.P - 1) / a.P : 0;
     for (int j = lane; j < pages; j += 32)
-        a.row_table[int64_t(row) * a.width + j] = a.table[int64_t(lo) * a.bt_stride + j];
+        a.row_table[int64_t(at) * a.width + j] = a.table[int64_t(lo) * a.bt_stride + j];
 }
 
-AttnShape rows_shape(const Layout &L, const CrossShape &s) {
+// The queries are taken some at a time, so that the workspace (prepared
+// queries, partial results, table rows) stays within some 100 MB whatever their
+// number: 65,536 rows of a head.
+int queries_at_once(const CrossShape &s) {
+    const int most = 65536 / s.Hq;
+    return s.total_q < most ? s.total_q : most > 1 ? most : 1;
+}
+
+AttnShape rows_shape(const Layout &L, const CrossShape &s, int n) {
     AttnShape r{};
-    r.n_seq = s.total_q;
+    r.n_seq = n;
     r.Hq = s.Hq;
     r.max_blocks = (s.max_kv_len + L.P - 1) / L.P;
     r.bt_stride = r.max_blocks;
@@ -65,9 +73,9 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // The size does not know the rotation of the parameters: it covers both ways.
 size_t cross_ws_bytes(const Layout &L, const CrossShape &s) {
-    const AttnShape r = rows_shape(L, s);
-    const size_t rows = up256(attn_ws_bytes(L, r)) + up256(4 * size_t(s.total_q)) +
-                        up256(4 * size_t(s.total_q) * size_t(r.max_blocks));
+    const int n = queries_at_once(s);
+    const AttnShape r = rows_shape(L, s, n);
+    const size_t rows = up256(attn_ws_bytes(L, r)) + up256(4 * size_t(n)) + up256(4 * size_t(n) * size_t(r.max_blocks));
     if (!cross_tc_covers(L, false, s)) return rows;
     const size_t tc = cross_tc_ws_bytes(L, s);
     return tc > rows ? tc : rows;
@@ -77,26 +85,35 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
                  const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream) {
     if (cross_tc_covers(L, kp->dev.rot || vp->dev.rot, s))
         return launch_cross_tc(kp, vp, L, Q, s, cache, num_blocks, out, lse, ws, static_cast<cudaStream_t>(stream));
-    AttnShape r = rows_shape(L, s);
+    const int n = queries_at_once(s);
+    AttnShape r = rows_shape(L, s, n);
     const size_t inner = up256(attn_ws_bytes(L, r));
     RowsArgs a;
     a.cu_q = s.cu_q;
     a.table = s.block_table;
     a.kv_lens = s.kv_lens;
     a.B = s.B;
-    a.total_q = s.total_q;
     a.max_q = s.max_q;
     a.bt_stride = s.max_blocks;
     a.max_kv_len = s.max_kv_len;
     a.P = L.P;
     a.width = r.max_blocks;
     a.row_len = reinterpret_cast<int32_t *>(ws + inner);
-    a.row_table = reinterpret_cast<int32_t *>(ws + inner + up256(4 * size_t(s.total_q)));
+    a.row_table = reinterpret_cast<int32_t *>(ws + inner + up256(4 * size_t(n)));
     a.status = reinterpret_cast<uint32_t *>(ws);
-    cross_rows_kernel<<<unsigned((s.total_q + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
     r.seq_lens = a.row_len;
     r.block_table = a.row_table;
-    return launch_attention(kp, vp, L, Q, r, cache, num_blocks, out, lse, nullptr, 0, ws, inner, stream);
+    for (int q0 = 0; q0 < s.total_q; q0 += n) {
+        a.row0 = q0;
+        a.n_rows = r.n_seq = s.total_q - q0 < n ? s.total_q - q0 : n;
+        cross_rows_kernel<<<unsigned((a.n_rows + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        const int64_t at = int64_t(q0) * s.Hq;
+        const int e = launch_attention(kp, vp, L, static_cast<const uint16_t *>(Q) + at * L.d, r, cache, num_blocks,
+                                       static_cast<uint16_t *>(out) + at * L.d, lse ? lse + at : nullptr, nullptr, 0, ws,
+                                       inner, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace tq

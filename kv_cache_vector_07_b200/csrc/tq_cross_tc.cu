@@ -567,7 +567,7 @@ struct AttendArgs {
     int n_splits, split_tiles;
     __nv_bfloat16 *out;
     float *lse;
-    float *part_o, *part_ml;               // [split][total_q Hq][D], [..][2]
+    float *part_o, *part_ml;               // [split][pair][max_q G][D], [..][2]
     uint32_t *status;
 };
 
@@ -577,6 +577,11 @@ __device__ __forceinline__ int run_of(const AttendArgs &a, int b, int *first, bo
     *first = q0;
     *cut = q0 >= 0 && q1 - q0 > a.max_q;
     return q0 >= 0 && q1 > q0 ? min(q1 - q0, a.max_q) : 0;
+}
+
+// Where the partial result of a pair's row i (position x heads + head) lies.
+__device__ __forceinline__ int64_t part_row(const AttendArgs &a, int split, int pl, int64_t i) {
+    return (int64_t(split) * gridDim.y + pl) * (int64_t(a.max_q) * a.G) + i;
 }
 
 // Unnormalised Walsh-Hadamard transform of a vector in registers.
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     const int qpos = pos0 + tt * a.PT + r / a.G;
     const bool row_ok = tid < 256 && r < a.PT * a.G && qpos < nq;
     const int64_t row = (int64_t(q0) + qpos) * a.Hq + h * a.G + r % a.G;
-    const int64_t prow = int64_t(split) * a.total_q * a.Hq + row;
+    const int64_t prow = part_row(a, split, pl, int64_t(qpos) * a.G + r % a.G);
 
     if (n <= 0) {                                         // no key of this split
         if (!row_ok) return;
@@ -989,19 +994,19 @@ template <int D>
 __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
-    const int pair = a.pair0 + blockIdx.y, b = pair / a.H, h = pair - b * a.H;
+    const int pl = int(blockIdx.y), pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H;
     const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
     int q0;
     bool cut;
     const int nq = run_of(a, b, &q0, &cut);
     if (i >= nq * a.G) return;
     const int64_t row = (int64_t(q0) + i / a.G) * a.Hq + h * a.G + i % a.G;
-    const int64_t step = int64_t(a.total_q) * a.Hq;
+    const int64_t first = part_row(a, 0, pl, i), step = part_row(a, 1, pl, i) - first;
     // lane s holds split s of a round of 32: the weights of all are there before
     // the first partial is asked for, and four partials are on their way at once
     float M = -INFINITY;
     for (int s = lane; s < a.n_splits; s += 32)
-        if (a.part_ml[(s * step + row) * 2 + 1] != 0.f) M = fmaxf(M, a.part_ml[(s * step + row) * 2]);
+        if (a.part_ml[(s * step + first) * 2 + 1] != 0.f) M = fmaxf(M, a.part_ml[(s * step + first) * 2]);
     M = warp_max(M);
     float l = 0.f, o[E];
 #pragma unroll
@@ -1010,9 +1015,9 @@ __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant_
         const int s = s0 + lane, n = min(32, a.n_splits - s0);
         float f = 0.f;                                    // 0: no key there
         if (s < a.n_splits) {
-            const float ls = a.part_ml[(s * step + row) * 2 + 1];
+            const float ls = a.part_ml[(s * step + first) * 2 + 1];
             if (ls != 0.f) {
-                f = exp2f(a.part_ml[(s * step + row) * 2] - M);
+                f = exp2f(a.part_ml[(s * step + first) * 2] - M);
                 l = fmaf(ls, f, l);
             }
         }
@@ -1023,7 +1028,7 @@ __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant_
                 w[k] = __shfl_sync(kFull, f, (i + k) & 31);
                 if (i + k >= n) w[k] = 0.f;
                 if (w[k] != 0.f) {
-                    load_vec<D>(a.part_o + ((s0 + i + k) * step + row) * D, lane, v[k]);
+                    load_vec<D>(a.part_o + ((s0 + i + k) * step + first) * D, lane, v[k]);
                 } else {
 #pragma unroll
                     for (int e = 0; e < E; ++e) v[k][e] = 0.f;
@@ -1080,7 +1085,7 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     p.off_order = take(size_t(p.round) * 4);
     p.off_meta = take(size_t(p.round) * p.n_tiles * sizeof(TileMeta));
     p.off_img = take(size_t(p.round) * pair_bytes);
-    const size_t rows = size_t(s.total_q) * s.Hq * p.n_splits;
+    const size_t rows = size_t(p.round) * size_t(s.max_q) * G * p.n_splits;
     p.off_po = take(p.n_splits > 1 ? rows * L.d * 4 : 0);
     p.off_pml = take(p.n_splits > 1 ? rows * 8 : 0);
     p.total = off;

@@ -490,8 +490,10 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
         raise ValueError("out must have Q's shape and dtype")
     if lse is not None and (lse.shape != (total_q, Hq) or lse.dtype is not torch.float32):
         raise ValueError("lse must be fp32 [total_q, Hq]")
-    if workspace is None:
-        workspace = _workspace(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), Q.device)
+    if workspace is None:                                # only its header (the status word) starts as zeros
+        workspace = torch.empty(max(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), 256),
+                                dtype=torch.uint8, device=Q.device)
+        workspace[:256].zero_()
     _call(dev, "tq_cross_attn", stream, kp.handle, vp.handle, ctypes.byref(desc), Q.data_ptr(), total_q, max_q, Hq,
           cu_q.data_ptr(), B, block_table.data_ptr(), block_table.size(1), kv_lens.data_ptr(), max_kv_len,
           cache.data_ptr(), cache.size(0), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())

@@ -212,6 +212,50 @@ def test_long_states_few_rows(codec):
 
 
 @pytest.mark.gpu
+def test_rows_behind_the_runs_of_a_split_call():
+    """The key axis is split and Q has many rows that belong to no run."""
+    c = Call(Codec(*CODECS["k5v4"], H=1), [30, 7], [5000, 3000], 4, seed=8, extra_rows=500)
+    out, lse, flags = c.run()
+    assert flags == 0
+    c.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_more_queries_than_one_round_by_rows():
+    """Head sizes that go by rows take 65,536 rows of a head at once."""
+    c = Call(Codec(*CODECS["d32"], H=8), [900, 600], [100, 64], 8, extra_rows=40)
+    out, lse, flags = c.run()
+    assert flags == 0
+    c.check(out, lse, rows=[0, 1, 500, 599, 899])
+
+
+@pytest.mark.gpu
+def test_more_states_than_one_round_holds():
+    """528 pairs of 64 tiles of 32 KB: the operand tiles take two rounds."""
+    kv = [8192] + [64] * 63 + [8190, 300]
+    c = Call(Codec(*CODECS["d64"], H=8), [7] + [0] * 62 + [2, 5, 9], kv, 1, seed=4)
+    out, lse, flags = c.run()
+    assert flags == 0
+    c.check(out, lse, rows=[0, 4, 8])
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """On two streams, with a workspace each."""
+    calls = [Call(Codec(*CODECS[n], H=2), [200, 90], [900, 1500], 4, seed=i) for i, n in enumerate(("k5v4", "k3v4"))]
+    want = [c.run()[0] for c in calls]
+    got = [torch.zeros_like(w) for w in want]
+    ws = [torch.zeros(tqkv.cross_workspace_bytes(c.cd.desc, 2, c.total, 200, 8, 1500), dtype=torch.uint8, device=DEV) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, o, w, st in zip(calls, got, ws, streams):
+            tqkv.cross_attn(*c.args, out=o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [2.0 ** -12, 2.0 ** 8])
 def test_small_and_large_states(scale):
     c = Call(Codec(*CODECS["k5v4"], H=1), [70], [500], 4, scale=scale)
@@ -327,7 +371,7 @@ def _c(desc=None, k=(128, 2), v=(128, 4), Q=256, total=8, max_q=4, Hq=4, cu=256,
     (dict(desc=tqkv.cache_desc(512, 2, True, 4)), tqkv.TQ_EUNSUPPORTED), (dict(Hq=18), tqkv.TQ_EUNSUPPORTED),
     (dict(Hq=3), tqkv.TQ_EINVAL), (dict(Hq=0), tqkv.TQ_EINVAL), (dict(total=-1), tqkv.TQ_EINVAL), (dict(max_q=-1), tqkv.TQ_EINVAL),
     (dict(B=-1), tqkv.TQ_EINVAL), (dict(maxkv=-1), tqkv.TQ_EINVAL), (dict(maxkv=257), tqkv.TQ_EINVAL),
-    (dict(total=1 << 30), tqkv.TQ_EINVAL), (dict(Q=None), tqkv.TQ_EINVAL), (dict(Q=264), tqkv.TQ_EINVAL),
+    (dict(total=1 << 30), tqkv.TQ_EINVAL), (dict(maxkv=2 ** 31 - 1, width=1 << 30), tqkv.TQ_EINVAL), (dict(Q=None), tqkv.TQ_EINVAL), (dict(Q=264), tqkv.TQ_EINVAL),
     (dict(cu=None), tqkv.TQ_EINVAL), (dict(table=None), tqkv.TQ_EINVAL), (dict(lens=None), tqkv.TQ_EINVAL),
     (dict(lens=2), tqkv.TQ_EINVAL), (dict(cache=128), tqkv.TQ_EINVAL), (dict(out=None), tqkv.TQ_EINVAL),
     (dict(lse=2), tqkv.TQ_EINVAL), (dict(ws=None), tqkv.TQ_EINVAL), (dict(ws=64), tqkv.TQ_EINVAL)])

@@ -375,6 +375,22 @@ def test_large_pool_is_searched_to_its_end():
 
 
 @pytest.mark.gpu
+def test_more_rows_and_requests_than_shared_memory_holds():
+    """The plans keep 1,024 requests and 4,096 rows on the chip, others in the workspace."""
+    p = Pair(d=8, kbits=1, vbits=0, P=8, H=1, layers=1, num_blocks=9000, n_rows=5000, max_blocks=3)
+    r = random.Random(1)
+    assert p.reserve([r.randint(0, 12) if i < 2500 else 0 for i in range(5000)]) == 0
+    src = [r.randrange(2500) for _ in range(1500)]
+    dst = r.sample(range(2490, 5000), 1500)                  # some of them in use
+    assert p.fork(src, dst) == tqkv.TQ_DEV_ROW
+    rows = r.sample(range(5000), 1300)
+    lists = [sorted(r.sample(range(int(p.m.lens[x])), r.randint(0, int(p.m.lens[x])))) for x in rows]
+    assert p.compact(rows, lists) == 0
+    assert p.free(list(range(5000))) == 0
+    assert (p.m.refs == 0).all()
+
+
+@pytest.mark.gpu
 def test_captured_calls_replay_on_the_state_they_find():
     p = Pair()
     p.reserve([20, 0, 0, 0, 0, 0, 0, 0])
