@@ -347,13 +347,13 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     // one ahead (one round of loads after another took 8,000 of an item's
     // 15,000 cycles)
     struct Place {
-        int there;                                     // 0: no such item, 1: key absent, 2: present
-        int pos;
-        const uint8_t *page;
+        bool item;                                     // there is such an item
+        int blk, pos, h;                               // -2: the key is behind the sequence
         unsigned image;                                // the tile's place in images and meta
     };
     struct Raw {
         Place at;
+        const uint8_t *page;                           // null: the key is absent
         uint16_t nk, nv, rk;
         uint32_t sign[D / 64];
         HalfBytes<D> k, v;
@@ -363,20 +363,21 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     // (stepping over the empty tiles of short sequences one by one cost as much
     // as a third of the tiles that hold something).
     const int last = a.pair0 + a.n_pairs;
-    int seq = a.pair0 / L.H, seq_tiles = 0, seq_first = a.pair0;
+    int seq = a.pair0 / L.H, seq_len = 0, seq_tiles = 0, seq_first = a.pair0;
     unsigned before_seq = 0, seq_items = 0;
     auto enter = [&](int b) {                          // sequence b and its pairs in this launch
         seq = b;
         seq_first = max(a.pair0, b * L.H);
         const int pairs = min(last, (b + 1) * L.H) - seq_first;
         if (pairs <= 0) return false;
-        seq_tiles = (min(max(a.kv_lens[b], 0), a.max_kv_len) + kTile - 1) / kTile;
+        seq_len = min(max(a.kv_lens[b], 0), a.max_kv_len);
+        seq_tiles = (seq_len + kTile - 1) / kTile;
         seq_items = unsigned(pairs) * unsigned(seq_tiles);
         return true;
     };
     bool more = enter(seq);
     auto place = [&](unsigned item) {
-        Place p{0, 0, nullptr, 0u};
+        Place p{false, -2, 0, 0, 0u};
         while (more && item - before_seq >= seq_items) {
             before_seq += seq_items;
             more = enter(seq + 1);
@@ -384,51 +385,47 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         if (!more) return p;
         const int within = int(item - before_seq), q = within / seq_tiles, tile = within - q * seq_tiles;
         const int pair = seq_first + q;
-        const int len = min(max(a.kv_lens[seq], 0), a.max_kv_len);
         const int t = tile * kTile + key, pg = t / L.P;
-        p.there = 1;
+        p.item = true;
         p.pos = t - pg * L.P;
+        p.h = pair - seq * L.H;
         p.image = unsigned(pair - a.pair0) * unsigned(a.n_tiles) + unsigned(tile);
-        if (t < len) {
-            const int blk = a.table[int64_t(seq) * a.bt_stride + pg];
-            if (blk >= 0 && blk < a.num_blocks) {
-                p.there = 2;
-                p.page = a.cache + (int64_t(blk) * L.H + (pair - seq * L.H)) * int64_t(L.page_bytes);
-            } else {
-                atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
-            }
-        }
+        if (t < seq_len) p.blk = a.table[int64_t(seq) * a.bt_stride + pg];   // looked at an item later
         return p;
     };
     auto fetch = [&](const Place &at) {
         Raw r;
         r.at = at;
+        r.page = nullptr;
         r.nk = r.nv = r.rk = 0;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) r.sign[i] = 0u;
-        if (at.there == 2) {
-            r.nk = *reinterpret_cast<const uint16_t *>(at.page + L.kn_off + at.pos * 2);
-            r.nv = *reinterpret_cast<const uint16_t *>(at.page + L.vn_off + at.pos * 2);
+        if (at.blk >= 0 && at.blk < a.num_blocks) {
+            const uint8_t *page = a.cache + (int64_t(at.blk) * L.H + at.h) * int64_t(L.page_bytes);
+            r.page = page;
+            r.nk = *reinterpret_cast<const uint16_t *>(page + L.kn_off + at.pos * 2);
+            r.nv = *reinterpret_cast<const uint16_t *>(page + L.vn_off + at.pos * 2);
             if (L.kqjl) {
-                r.rk = *reinterpret_cast<const uint16_t *>(at.page + L.kr_off + at.pos * 2);
+                r.rk = *reinterpret_cast<const uint16_t *>(page + L.kr_off + at.pos * 2);
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
-                    r.sign[i] =
-                        reinterpret_cast<const uint32_t *>(at.page + L.ks_off + at.pos * L.ks_bpt + hh * (HALF / 8))[i];
+                    r.sign[i] = reinterpret_cast<const uint32_t *>(page + L.ks_off + at.pos * L.ks_bpt + hh * (HALF / 8))[i];
             }
-            fetch_codes<D>(kc, at.page, at.pos, r.k);
-            fetch_codes<D>(vc, at.page, at.pos, r.v);
+            fetch_codes<D>(kc, page, at.pos, r.k);
+            fetch_codes<D>(vc, page, at.pos, r.v);
+        } else if (at.blk != -2) {
+            atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
         }
         return r;
     };
     Raw coming = fetch(place(blockIdx.x));
     Place ahead = place(blockIdx.x + gridDim.x);
-    for (unsigned item = blockIdx.x; coming.at.there && !timeout; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; coming.at.item && !timeout; item += gridDim.x) {
         const Raw raw = coming;
         coming = fetch(ahead);
         ahead = place(item + 2 * gridDim.x);
         const int pos = raw.at.pos;
-        const uint8_t *page = raw.at.page;
+        const uint8_t *page = raw.page;
         const float nk = h2f_bits(raw.nk), nv = h2f_bits(raw.nv), rk = cq * h2f_bits(raw.rk);
         if (tid == 0) bulk_wait_read();                // the tiles of the item before have been read
         // a key's coordinate is below bound nk + rk sum_j |S_ji|, and |S_ji| below
