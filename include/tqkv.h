@@ -402,7 +402,9 @@ int tq_pages_compact(const tq_cache_desc *desc, const tq_page_pool *pool, void *
                      void *workspace, size_t workspace_bytes, void *stream);
 
 /* Rows rows[0 .. n) give their pages back and become empty (an empty row, or
- * one named twice, gives nothing more). */
+ * one named twice, gives nothing more).  Broken rows become empty, too: of one
+ * that lists pages out of range or free the others are given back
+ * (TQ_DEV_BLOCK_RANGE), of one with an impossible length none (TQ_DEV_ROW). */
 int tq_pages_free(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *rows, int n, void *workspace,
                   size_t workspace_bytes, void *stream);
 

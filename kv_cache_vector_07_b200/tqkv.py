@@ -10,6 +10,7 @@ not pass one; the library itself never allocates device memory outside
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -292,6 +293,17 @@ def cache_bytes(desc: CacheDesc) -> int:
     return int(out.value)
 
 
+def _made_on(dev: int, stream):
+    """Context for the tensors that a call makes itself: what clears them, and
+    the allocator's reuse of them, are ordered by the stream the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        at = int(stream)
+        stream = torch.cuda.ExternalStream(at, device=dev) if at else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 @functools.lru_cache(maxsize=256)
 def _page_bytes(*fields) -> int:
     return cache_bytes(CacheDesc(*fields))
@@ -485,15 +497,17 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
     if cache.dim() != 3 or not _is_cache(cache, cache.size(0), desc.n_kv_heads, _page_of(desc)):
         raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
     if out is None:
-        out = torch.zeros_like(Q)
+        with _made_on(dev, stream):
+            out = torch.zeros_like(Q)
     elif out.shape != Q.shape or out.dtype is not Q.dtype:
         raise ValueError("out must have Q's shape and dtype")
     if lse is not None and (lse.shape != (total_q, Hq) or lse.dtype is not torch.float32):
         raise ValueError("lse must be fp32 [total_q, Hq]")
     if workspace is None:                                # only its header (the status word) starts as zeros
-        workspace = torch.empty(max(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), 256),
-                                dtype=torch.uint8, device=Q.device)
-        workspace[:256].zero_()
+        with _made_on(dev, stream):
+            workspace = torch.empty(max(cross_workspace_bytes(desc, B, total_q, max_q, Hq, max_kv_len), 256),
+                                    dtype=torch.uint8, device=Q.device)
+            workspace[:256].zero_()
     _call(dev, "tq_cross_attn", stream, kp.handle, vp.handle, ctypes.byref(desc), Q.data_ptr(), total_q, max_q, Hq,
           cu_q.data_ptr(), B, block_table.data_ptr(), block_table.size(1), kv_lens.data_ptr(), max_kv_len,
           cache.data_ptr(), cache.size(0), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
@@ -507,7 +521,7 @@ def pages_workspace_bytes(num_blocks: int, n_rows: int, max_blocks: int) -> int:
     return int(_lib.tq_pages_workspace_bytes(num_blocks, n_rows, max_blocks))
 
 
-def _pool(desc, refs, table, lens, ints, workspace, caches=None):
+def _pool(desc, refs, table, lens, ints, workspace, stream, caches=None):
     """(device index, tq_page_pool, workspace, cache pointers) of a pages call."""
     dev = _one_device(refs, table, lens, workspace, *ints)
     for t in (refs, table, lens, *ints):
@@ -529,7 +543,8 @@ def _pool(desc, refs, table, lens, ints, workspace, caches=None):
         if not ptrs:
             raise ValueError("caches must name one cache at least")
     if workspace is None:
-        workspace = _workspace(pages_workspace_bytes(num_blocks, n_rows, max_blocks), refs.device)
+        with _made_on(dev, stream):
+            workspace = _workspace(pages_workspace_bytes(num_blocks, n_rows, max_blocks), refs.device)
     pool = _PagePool(refs.data_ptr(), table.data_ptr(), lens.data_ptr(), num_blocks, n_rows, max_blocks)
     return dev, pool, workspace, ptrs
 
@@ -541,7 +556,7 @@ def pages_reserve(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens
     tokens of every row; slot_mapping int32 [n_slots] receives their slots, row
     after row.  refs int32 [num_blocks], table int32 [n_rows, max_blocks] and
     lens int32 [n_rows] are updated.  Returns the workspace (read_status)."""
-    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (new_tokens, slot_mapping), workspace)
+    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (new_tokens, slot_mapping), workspace, stream)
     if new_tokens.shape != lens.shape or slot_mapping.dim() != 1:
         raise ValueError("new_tokens must be [n_rows] and slot_mapping [n_slots]")
     _call(dev, "tq_pages_reserve", stream, ctypes.byref(desc), ctypes.byref(pool), new_tokens.data_ptr(),
@@ -555,7 +570,7 @@ def pages_fork(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tensor,
     """tq_pages_fork: rows dst_rows (empty) become copies of rows src_rows
     (int32 [n]); caches: one cache, or a list with every layer's.  Full pages
     are shared, partly filled ones copied.  Returns the workspace."""
-    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (src_rows, dst_rows), workspace, caches)
+    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (src_rows, dst_rows), workspace, stream, caches)
     if src_rows.dim() != 1 or src_rows.shape != dst_rows.shape:
         raise ValueError("src_rows and dst_rows must be [n]")
     _call(dev, "tq_pages_fork", stream, ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), src_rows.data_ptr(),
@@ -569,7 +584,7 @@ def pages_compact(desc: CacheDesc, caches, refs: torch.Tensor, table: torch.Tens
     """tq_pages_compact: row rows[i] keeps its tokens keep[i, :keep_lens[i]]
     (int32 [n], [n, most], [n]), in that order; caches as in pages_fork.
     Returns the workspace."""
-    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (rows, keep, keep_lens), workspace, caches)
+    dev, pool, workspace, ptrs = _pool(desc, refs, table, lens, (rows, keep, keep_lens), workspace, stream, caches)
     if rows.dim() != 1 or keep.dim() != 2 or keep.size(0) != rows.numel() or keep_lens.shape != rows.shape:
         raise ValueError("rows and keep_lens must be [n] and keep [n, most]")
     _call(dev, "tq_pages_compact", stream, ctypes.byref(desc), ctypes.byref(pool), ptrs, len(ptrs), rows.data_ptr(),
@@ -581,7 +596,7 @@ def pages_free(desc: CacheDesc, refs: torch.Tensor, table: torch.Tensor, lens: t
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """tq_pages_free: rows (int32 [n]) give their pages back and become empty.
     Returns the workspace."""
-    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (rows,), workspace)
+    dev, pool, workspace, _ = _pool(desc, refs, table, lens, (rows,), workspace, stream)
     if rows.dim() != 1:
         raise ValueError("rows must be [n]")
     _call(dev, "tq_pages_free", stream, ctypes.byref(desc), ctypes.byref(pool), rows.data_ptr(), rows.numel(),
@@ -606,14 +621,15 @@ def rope_desc(d: int, rot_dim: int | None = None, style: int = TQ_ROPE_HALF, pai
 _ROPE_DTYPES = {torch.bfloat16: TQ_DTYPE_BF16, torch.float32: TQ_DTYPE_F32}
 
 
-def _heads(x, weight, out, d, n, name):
+def _heads(x, weight, out, d, n, name, dev, stream):
     """(tq_heads, result tensor) of one side of qk_norm_rope."""
     if x is None:
         return None, None
     if x.dim() != 3 or x.size(0) != n or x.size(2) != d:
         raise ValueError(f"{name} must be [n_tokens, heads, d]")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        with _made_on(dev, stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError(f"{name}_out must have {name}'s shape and dtype")
     (xt, xh, xd), (ot, oh, od) = x.stride(), out.stride()
@@ -654,8 +670,8 @@ def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None,
         raise ValueError("positions must be [n_tokens], or [n_axes, n_tokens], with adjacent tokens")
     if inv_freq.numel() != desc.rot_dim // 2 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous [rot_dim / 2]")
-    hq, q_out = _heads(q, q_weight, q_out, desc.d, n, "q")
-    hk, k_out = _heads(k, k_weight, k_out, desc.d, n, "k")
+    hq, q_out = _heads(q, q_weight, q_out, desc.d, n, "q", dev, stream)
+    hk, k_out = _heads(k, k_weight, k_out, desc.d, n, "k", dev, stream)
     _call(dev, "tq_qk_norm_rope", stream, ctypes.byref(desc), dt, wt, n, None if hq is None else ctypes.byref(hq),
           None if hk is None else ctypes.byref(hk), positions.data_ptr(), positions.stride(0) if axes == 2 else n,
           inv_freq.data_ptr())

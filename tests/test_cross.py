@@ -256,6 +256,35 @@ def test_two_calls_at_once():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("codec", ["k5v4", "k3v4"])
+@pytest.mark.parametrize("as_number", [False, True])
+def test_what_the_call_makes_belongs_to_its_stream(codec, as_number):
+    """out and workspace not given, the current stream busy: what clears them
+    must not come behind the call's own kernels."""
+    c = Call(Codec(*CODECS[codec], H=2), [3, 1] if codec == "k3v4" else [70, 9], [300, 500], 4)
+    want = c.run()[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.zeros(1 << 28, dtype=torch.uint8, device=DEV)
+    for _ in range(40):                                              # some milliseconds of work
+        busy += 1
+    got = tqkv.cross_attn(*c.args, stream=side.cuda_stream if as_number else side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+def test_any_number_out_of_range_is_reported(page):
+    for qlens in ([2, 1], [70, 40]):
+        c = Call(Codec(*CODECS["k3v4"], H=2), qlens, [300, 200], 2)
+        c.table[1, 3] = page                                         # tokens 192 .. 199
+        out, lse, flags = c.run()
+        assert flags == tqkv.TQ_DEV_BLOCK_RANGE
+        c.check(out, lse, missing={1: np.arange(200) >= 192})
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [2.0 ** -12, 2.0 ** 8])
 def test_small_and_large_states(scale):
     c = Call(Codec(*CODECS["k5v4"], H=1), [70], [500], 4, scale=scale)

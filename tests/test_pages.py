@@ -343,6 +343,23 @@ def test_tables_that_are_broken_are_reported():
 
 
 @pytest.mark.gpu
+def test_workspace_it_makes_belongs_to_its_stream():
+    p, q = Pair(), Pair()
+    new, slots = p.ints([20, 33, 0, 1, 0, 0, 0, 5]), torch.zeros(59, dtype=torch.int32, device=DEV)
+    tqkv.pages_reserve(p.desc, *p.state, new, slots)
+    side, other = torch.cuda.Stream(), torch.zeros_like(slots)
+    busy = torch.zeros(1 << 28, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(40):                                                   # a cleared workspace would come behind these
+        busy += 1
+    ws = tqkv.pages_reserve(q.desc, *q.state, new, other, stream=side)
+    side.synchronize()
+    assert tqkv.read_status(ws, side) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(slots, other) and all(torch.equal(a, b) for a, b in zip(p.state, q.state))
+
+
+@pytest.mark.gpu
 def test_many_layers_and_no_requests():
     p = Pair(d=8, kbits=1, vbits=1, P=8, H=1, layers=131, num_blocks=9, n_rows=3, max_blocks=3)
     assert p.reserve([13, 0, 0]) == 0

@@ -149,6 +149,26 @@ def test_empty_zero_and_non_finite_vectors():
 
 
 @pytest.mark.gpu
+def test_results_it_makes_belong_to_its_stream():
+    """Room that the current stream still writes to is not given to a call on another one."""
+    n, d = 4096, 128
+    q, k, w = inputs(n, 8, 2, d, torch.bfloat16, 9)
+    pos = torch.arange(n, device=DEV, dtype=torch.int32)
+    inv, rd = frequencies(64), tqkv.rope_desc(d)
+    ref = [t.clone() for t in tqkv.qk_norm_rope(rd, q, k, pos, inv, w[0], w[1])]
+    side = torch.cuda.Stream()
+    busy, room = torch.zeros(1 << 28, dtype=torch.uint8, device=DEV), torch.empty_like(ref[0])
+    torch.cuda.synchronize()
+    for _ in range(40):
+        busy += 1
+    room.fill_(3.0)
+    del room                                                 # its writer waits behind the others
+    got = tqkv.qk_norm_rope(rd, q, k, pos, inv, w[0], w[1], stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.gpu
 def test_stream_and_graph_replay():
     n, d = 50, 128
     q, k, w = inputs(n, 8, 2, d, torch.bfloat16, 9)
