@@ -187,13 +187,15 @@ def _dev_check(*tensors):
 
 def _one_device(*tensors) -> int:
     """The index of the one CUDA device that all given tensors are on."""
-    dev = -1
+    dev = None
     for t in tensors:
         if t is not None:
-            at = t.get_device()
-            if at < 0 or (dev >= 0 and at != dev):
+            if dev is None:
+                dev = t.get_device()
+            elif t.get_device() != dev:
+                dev = -1
+            if dev < 0:
                 raise ValueError("libtqkv arguments must be CUDA tensors of one device")
-            dev = at
     return dev
 
 
@@ -205,7 +207,7 @@ def _call(dev: int, name: str, stream, *args):
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     f = getattr(_lib, name)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         code = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -312,10 +314,6 @@ def _page_bytes(*fields) -> int:
 def _page_of(desc: CacheDesc) -> int:
     """cache_bytes, remembered by the description's values."""
     return _page_bytes(desc.d, desc.kbits, desc.kqjl, desc.vbits, desc.page_tokens, desc.n_kv_heads)
-
-
-def _is_cache(c: torch.Tensor, num_blocks: int, heads: int, page: int) -> bool:
-    return c.dtype is torch.uint8 and c.is_contiguous() and c.shape == (num_blocks, heads, page)
 
 
 def alloc_cache(desc: CacheDesc, num_blocks: int, device="cuda") -> torch.Tensor:
@@ -494,7 +492,8 @@ def cross_attn(kp: Params, vp: Params, desc: CacheDesc, Q: torch.Tensor, cu_q: t
         raise ValueError("block_table must be [B, max_blocks], kv_lens [B] and cu_q [B + 1]")
     if not (cu_q.dtype is block_table.dtype is kv_lens.dtype is torch.int32):
         raise ValueError("cu_q, block_table and kv_lens must be int32")
-    if cache.dim() != 3 or not _is_cache(cache, cache.size(0), desc.n_kv_heads, _page_of(desc)):
+    if cache.dtype is not torch.uint8 or cache.shape[1:] != (desc.n_kv_heads, _page_of(desc)) or \
+            not cache.is_contiguous():
         raise ValueError("cache must be uint8 [num_blocks, n_kv_heads, page bytes]")
     if out is None:
         with _made_on(dev, stream):
@@ -527,21 +526,21 @@ def _pool(desc, refs, table, lens, ints, workspace, stream, caches=None):
     for t in (refs, table, lens, *ints):
         if t.dtype is not torch.int32 or not t.is_contiguous():
             raise ValueError("refs, table, lens and the requests must be contiguous int32 tensors")
-    if refs.dim() != 1 or table.dim() != 2 or lens.dim() != 1 or lens.numel() != table.size(0):
+    shape = table.shape
+    if len(shape) != 2 or refs.dim() != 1 or lens.shape != shape[:1]:
         raise ValueError("refs must be [num_blocks], table [n_rows, max_blocks] and lens [n_rows]")
-    num_blocks, (n_rows, max_blocks) = refs.numel(), table.shape
+    num_blocks, (n_rows, max_blocks) = refs.size(0), shape
     ptrs = None
     if caches is not None:
         layers = [caches] if isinstance(caches, torch.Tensor) else caches
-        page = _page_of(desc)
-        ptrs = (_vp * len(layers))()
-        for i, c in enumerate(layers):
-            if c.get_device() != dev or not _is_cache(c, num_blocks, desc.n_kv_heads, page):
+        want = (num_blocks, desc.n_kv_heads, _page_of(desc))
+        for c in layers:
+            if c.get_device() != dev or c.dtype is not torch.uint8 or c.shape != want or not c.is_contiguous():
                 raise ValueError("every cache must be contiguous uint8 [num_blocks, n_kv_heads, page bytes] on the "
                                  "tables' device")
-            ptrs[i] = c.data_ptr()
-        if not ptrs:
+        if not layers:
             raise ValueError("caches must name one cache at least")
+        ptrs = (_vp * len(layers))(*[c.data_ptr() for c in layers])
     if workspace is None:
         with _made_on(dev, stream):
             workspace = _workspace(pages_workspace_bytes(num_blocks, n_rows, max_blocks), refs.device)
@@ -625,18 +624,20 @@ def _heads(x, weight, out, d, n, name, dev, stream):
     """(tq_heads, result tensor) of one side of qk_norm_rope."""
     if x is None:
         return None, None
-    if x.dim() != 3 or x.size(0) != n or x.size(2) != d:
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d:
         raise ValueError(f"{name} must be [n_tokens, heads, d]")
     if out is None:
         with _made_on(dev, stream):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype is not x.dtype:
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif out.shape != shape or out.dtype is not x.dtype:
         raise ValueError(f"{name}_out must have {name}'s shape and dtype")
-    (xt, xh, xd), (ot, oh, od) = x.stride(), out.stride()
+    xt, xh, xd = x.stride()
+    ot, oh, od = out.stride()
     if xd != 1 or od != 1:
         raise ValueError(f"the coordinates of {name} and {name}_out must be adjacent")
     return _Heads(x.data_ptr(), xt, xh, None if weight is None else weight.data_ptr(), out.data_ptr(), ot, oh,
-                  x.size(1)), out
+                  shape[1]), out
 
 
 def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
@@ -649,31 +650,31 @@ def qk_norm_rope(desc: RopeDesc, q: torch.Tensor | None, k: torch.Tensor | None,
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    n = x.size(0)
+    d, n = desc.d, x.size(0)
     dev = _one_device(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    dt = _ROPE_DTYPES.get(x.dtype)
-    if dt is None or (k is not None and k.dtype is not x.dtype):
+    dtype, wtype = x.dtype, None
+    if dtype not in _ROPE_DTYPES or (k is not None and k.dtype is not dtype):
         raise ValueError("q and k must both be bf16 or both fp32")
-    wt = dt
     for w in (q_weight, k_weight):
         if w is not None:
-            wt = _ROPE_DTYPES.get(w.dtype)
-            if wt is None or w.dim() != 1 or w.numel() != desc.d or not w.is_contiguous():
+            if wtype is not None and w.dtype is not wtype:
+                raise ValueError("the weights must both be bf16 or both fp32")
+            wtype = w.dtype
+            if wtype not in _ROPE_DTYPES or w.shape != (d,) or not w.is_contiguous():
                 raise ValueError("weights must be contiguous [d], bf16 or fp32")
-    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
-        raise ValueError("the weights must both be bf16 or both fp32")
     if positions.dtype is not torch.int32 or inv_freq.dtype is not torch.float32:
         raise ValueError("positions must be int32 and inv_freq fp32")
-    axes = positions.dim()
-    if axes not in (1, 2) or positions.size(-1) != n or (positions.size(0) if axes == 2 else 1) != desc.n_axes or \
-            (n > 1 and positions.stride(-1) != 1):
-        raise ValueError("positions must be [n_tokens], or [n_axes, n_tokens], with adjacent tokens")
+    shape, step = positions.shape, positions.stride()
+    if shape != (n,) if desc.n_axes == 1 and len(shape) == 1 else shape != (desc.n_axes, n):
+        raise ValueError("positions must be [n_tokens], or [n_axes, n_tokens]")
+    if n > 1 and step[-1] != 1:
+        raise ValueError("the positions of an axis must be adjacent")
     if inv_freq.numel() != desc.rot_dim // 2 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous [rot_dim / 2]")
-    hq, q_out = _heads(q, q_weight, q_out, desc.d, n, "q", dev, stream)
-    hk, k_out = _heads(k, k_weight, k_out, desc.d, n, "k", dev, stream)
-    _call(dev, "tq_qk_norm_rope", stream, ctypes.byref(desc), dt, wt, n, None if hq is None else ctypes.byref(hq),
-          None if hk is None else ctypes.byref(hk), positions.data_ptr(), positions.stride(0) if axes == 2 else n,
+    hq, q_out = _heads(q, q_weight, q_out, d, n, "q", dev, stream)
+    hk, k_out = _heads(k, k_weight, k_out, d, n, "k", dev, stream)
+    _call(dev, "tq_qk_norm_rope", stream, ctypes.byref(desc), _ROPE_DTYPES[dtype], _ROPE_DTYPES[wtype or dtype], n,
+          hq and ctypes.byref(hq), hk and ctypes.byref(hk), positions.data_ptr(), step[0] if len(shape) == 2 else n,
           inv_freq.data_ptr())
     return q_out, k_out
 
