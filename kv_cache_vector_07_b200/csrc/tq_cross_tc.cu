@@ -77,6 +77,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -588,16 +598,28 @@ __device__ __forceinline__ int64_t part_row(const AttendArgs &a, int split, int 
 
 // Unnormalised Walsh-Hadamard transform of a vector in registers.
 template <int D>
-__device__ __forceinline__ void fwht_regs(float (&x)[D]) {
+__device__ __forceinline__ void fwht_regs(float2 (&x)[D / 2]) {
 #pragma unroll
-    for (int s = 1; s < D; s <<= 1)
+    for (int i = 0; i < D / 2; ++i) x[i] = make_float2(x[i].x + x[i].y, x[i].x - x[i].y);
 #pragma unroll
-        for (int i = 0; i < D; ++i)
+    for (int s = 1; s < D / 2; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
             if ((i & s) == 0) {
-                const float u = x[i], v = x[i + s];
-                x[i] = u + v;
-                x[i + s] = u - v;
+                const float2 u = x[i], v = x[i + s];
+                x[i] = add2(u, v);
+                x[i + s] = fma2(v, make_float2(-1.f, -1.f), u);
             }
+}
+// x *= the signs of a rotation.
+template <int D>
+__device__ __forceinline__ void sign_regs(float2 (&x)[D / 2], const float *signs) {
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) {
+        const float4 s = reinterpret_cast<const float4 *>(signs)[i];
+        x[2 * i] = mul2(x[2 * i], make_float2(s.x, s.y));
+        x[2 * i + 1] = mul2(x[2 * i + 1], make_float2(s.z, s.w));
+    }
 }
 
 template <int D>
@@ -829,7 +851,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
         float rowc = 1.f;
         bool finite = true;
         {
-            float x[D];
+            float2 x[D / 2];
             if (row_ok) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(a.Q + row * D);
 #pragma unroll
@@ -837,33 +859,40 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
                     const uint4 u = src[c];
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[8 * c + 2 * e] = __uint_as_float(w[e] << 16) * a.ksigns[8 * c + 2 * e];
-                        x[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * a.ksigns[8 * c + 2 * e + 1];
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        x[4 * c + e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < D; ++i) x[i] = 0.f;
+                for (int i = 0; i < D / 2; ++i) x[i] = make_float2(0.f, 0.f);
             }
+            sign_regs<D>(x, a.ksigns);
             fwht_regs<D>(x);
-            float mx = 0.f, bad = 0.f;
+            float mx = 0.f;
+            float2 bad = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < D; ++i) {
-                mx = fmaxf(mx, fabsf(x[i]));
-                bad += x[i] * 0.f;
+            for (int i = 0; i < D / 2; ++i) {
+                mx = fmaxf(mx, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+                bad = fma2(x[i], make_float2(0.f, 0.f), bad);
             }
-            finite = bad == 0.f;                           // a coordinate that is not finite spreads over the row
+            finite = bad.x + bad.y == 0.f;                 // a coordinate that is not finite spreads over the row
             int e;
             const float down = scale_to(finite ? mx : 0.f, 11, &e);
             // log2(e) / sqrt(d) of the logit, 1 / sqrt(d) of the rotation
             rowc = ldexpf(1.4426950408889634f / float(D), e);
             uint8_t *dst = sQ + uint32_t(tt) * kImg;
+            const float2 down2 = make_float2(down, down);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 y = mul2(x[4 * c + k], down2);
+                    w[k] = h2u(y.x, y.y);
+                }
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + tc05::sw128_offset(uint32_t(r), uint32_t(c & 7))) =
-                    make_uint4(h2u(x[8 * c] * down, x[8 * c + 1] * down), h2u(x[8 * c + 2] * down, x[8 * c + 3] * down),
-                               h2u(x[8 * c + 4] * down, x[8 * c + 5] * down), h2u(x[8 * c + 6] * down, x[8 * c + 7] * down));
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
         tc05::fence_proxy_async_smem();
         __syncwarp();
@@ -951,29 +980,31 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
         if (!timeout && !wait_w(&o_done[tt], 0u)) timeout = true;
         tc05::fence_after_sync();
         if (!finite) l = __uint_as_float(0x7FC00000u);
-        float o[D];
+        uint32_t raw[D];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
-            tc05::tmem_ld_32x32b_x32(to + uint32_t(c * 32), reinterpret_cast<uint32_t(&)[32]>(o[c * 32]));
+            tc05::tmem_ld_32x32b_x32(to + uint32_t(c * 32), reinterpret_cast<uint32_t(&)[32]>(raw[c * 32]));
         tc05::tmem_wait_ld();
+        float2 o[D / 2];
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) o[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
         if (row_ok && a.n_splits > 1) {
             float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D);
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
             a.part_ml[prow * 2] = m;
             a.part_ml[prow * 2 + 1] = l;
         } else if (row_ok) {
             fwht_regs<D>(o);
             const float inv = (l != l || l > 0.f ? 1.f / l : 0.f) * rsqrtf(float(D));
+            sign_regs<D>(o, a.vsigns);
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 8 * c + 2 * e;
-                    const __nv_bfloat162 v =
-                        __floats2bfloat162_rn(o[i] * inv * a.vsigns[i], o[i + 1] * inv * a.vsigns[i + 1]);
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(o[4 * c + e].x * inv, o[4 * c + e].y * inv);
                     w[e] = *reinterpret_cast<const uint32_t *>(&v);
                 }
                 dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
