@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "tc05.cuh"
+#include "tq_chain.cuh"
 #include "tq_dev.cuh"
 
 namespace tq {
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int key = tid & 127, hh = tid >> 7;
 
+    let_next_in();
     if (blockIdx.x == 0) order_pairs(a);
     // S as the B operand: row j holds S[j][0 .. D), 64 columns to a half
     if (L.kqjl) {
@@ -642,6 +644,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     constexpr uint32_t kImg = uint32_t(image_bytes(D));
     constexpr int NS = ring_slots<D>();
     constexpr uint32_t TO = 256;                          // TMEM columns: S / P of the tiles at 0 and 128, O behind
+    wait_for_last();
+    let_next_in();
     const int pl = a.order[blockIdx.y], pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H, split = blockIdx.z;
     int q0;
     bool cut;
@@ -1026,6 +1030,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
 template <int D>
 __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int E = D / 32;
+    wait_for_last();
     const int lane = threadIdx.x & 31;
     const int pl = int(blockIdx.y), pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H;
     const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
@@ -1190,10 +1195,12 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
         x.n_pairs = np;
         const int64_t items = int64_t(np) * p.n_tiles;
         cross_expand_kernel<D><<<unsigned(items < 296 ? items : 296), 256, expand_smem<D>(), st>>>(x);
-        cross_attend_kernel<D><<<dim3(unsigned(p.x), unsigned(np), unsigned(p.n_splits)), kAttendThreads,
-                                 attend_smem<D>(), st>>>(a);
-        if (p.n_splits > 1)
-            cross_merge_kernel<D><<<dim3(unsigned((int64_t(s.max_q) * a.G + 3) / 4), unsigned(np)), 128, 0, st>>>(a);
+        e = launch_next(cross_attend_kernel<D>, dim3(unsigned(p.x), unsigned(np), unsigned(p.n_splits)), kAttendThreads,
+                        attend_smem<D>(), st, a);
+        if (e == cudaSuccess && p.n_splits > 1)
+            e = launch_next(cross_merge_kernel<D>, dim3(unsigned((int64_t(s.max_q) * a.G + 3) / 4), unsigned(np)), 128, 0,
+                            st, a);
+        if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
 }

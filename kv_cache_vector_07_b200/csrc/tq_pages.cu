@@ -13,6 +13,7 @@
 
 #include <cuda_runtime.h>
 
+#include "tq_chain.cuh"
 #include "tq_dev.cuh"
 
 namespace tq {
@@ -180,6 +181,7 @@ __device__ __forceinline__ bool row_lives(const PoolArgs &a, int r, int pages) {
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(PoolArgs a, const int32_t *src, const int32_t *dst,
                                                                  int n) {
     __shared__ PlanShared sh;
+    let_next_in();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool few = n <= kSharedRequests;
     int32_t *need = few ? sh.need : a.ws.need, *start = few ? sh.start : a.ws.start, *lens = few ? sh.len : a.ws.old;
@@ -250,6 +252,7 @@ struct Layers {
 // Job's page copied in layer blockIdx.y; blockIdx.z takes a slice of it.
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ Layers layers, PlanWs ws,
                                                          int64_t block_bytes) {
+    wait_for_last();
     if (int(blockIdx.x) >= *ws.n_jobs) return;
     const int4 job = ws.jobs[blockIdx.x];
     uint8_t *base = layers.at[blockIdx.y];
@@ -383,6 +386,7 @@ __host__ __device__ __forceinline__ int pages_kept(const PoolArgs &a, int keep_s
 // eight of 4,095 took it 32 of its 43 us).
 __global__ void __launch_bounds__(256) compact_look_kernel(PoolArgs a, const int32_t *rows, const int32_t *keep,
                                                            int keep_stride, const int32_t *keep_lens, int n) {
+    let_next_in();
     const int lane = threadIdx.x & 31, most = pages_kept(a, keep_stride);
     const int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int i = int(w / most), j = int(w - int64_t(i) * most);
@@ -406,6 +410,8 @@ __global__ void __launch_bounds__(256) compact_look_kernel(PoolArgs a, const int
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolArgs a, const int32_t *rows,
                                                                     int keep_stride, const int32_t *keep_lens, int n) {
     __shared__ PlanShared sh;
+    wait_for_last();
+    let_next_in();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool few = n <= kSharedRequests;
     // lens: the rows' lengths; out: a kept token is out of range (start's room,
@@ -554,6 +560,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                                                                 const __grid_constant__ GatherArgs a) {
     __shared__ int64_t from[256];                    // byte of the token's page
     __shared__ int slot[256];                        // and its position there
+    wait_for_last();
     const int n_jobs = *a.ws.n_jobs, groups = (a.H + a.heads - 1) / a.heads;
     const int64_t page_stride = int64_t(a.H) * a.page_bytes;
     for (int64_t w = blockIdx.x; w < int64_t(n_jobs) * groups; w += gridDim.x) {
@@ -630,7 +637,9 @@ int launch_pages_fork(const Layout &L, const tq_page_pool &pool, void *const *ca
     const unsigned z = unsigned(bytes / 16384 < 1 ? 1 : bytes / 16384 > 64 ? 64 : bytes / 16384);
     for (int l0 = 0; l0 < n_layers; l0 += kLayersPerLaunch) {
         const int nl = n_layers - l0 < kLayersPerLaunch ? n_layers - l0 : kLayersPerLaunch;
-        copy_pages_kernel<<<dim3(unsigned(n), unsigned(nl), z), 256, 0, st>>>(layers_of(caches + l0, nl), a.ws, bytes);
+        const cudaError_t e = launch_next(copy_pages_kernel, dim3(unsigned(n), unsigned(nl), z), 256, 0, st,
+                                          layers_of(caches + l0, nl), a.ws, bytes);
+        if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
 }
@@ -654,8 +663,14 @@ int launch_pages_compact(const Layout &L, const tq_page_pool &pool, void *const 
     const PoolArgs a = pool_args(L, pool, ws);
     const int64_t lists = (int64_t(n) * pages_kept(a, keep_stride) + 7) / 8;
     if (lists > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (lists > 0) compact_look_kernel<<<unsigned(lists), 256, 0, st>>>(a, rows, keep, keep_stride, keep_lens, n);
-    compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, rows, keep_stride, keep_lens, n);
+    cudaError_t e = cudaSuccess;
+    if (lists > 0) {
+        compact_look_kernel<<<unsigned(lists), 256, 0, st>>>(a, rows, keep, keep_stride, keep_lens, n);
+        e = launch_next(compact_plan_kernel, dim3(1), kPlanThreads, 0, st, a, rows, keep_stride, keep_lens, n);
+    } else {
+        compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, rows, keep_stride, keep_lens, n);
+    }
+    if (e != cudaSuccess) return e;
     GatherArgs g{};
     g.ws = a.ws;
     g.keep = keep;
@@ -697,7 +712,8 @@ int launch_pages_compact(const Layout &L, const tq_page_pool &pool, void *const 
     const unsigned x = unsigned(most < 1 ? 1 : most > 65536 ? 65536 : most);
     for (int l0 = 0; l0 < n_layers; l0 += kLayersPerLaunch) {
         const int nl = n_layers - l0 < kLayersPerLaunch ? n_layers - l0 : kLayersPerLaunch;
-        gather_kernel<<<dim3(x, unsigned(nl)), kGatherThreads, 0, st>>>(layers_of(caches + l0, nl), g);
+        e = launch_next(gather_kernel, dim3(x, unsigned(nl)), kGatherThreads, 0, st, layers_of(caches + l0, nl), g);
+        if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
 }
