@@ -13,6 +13,7 @@
 // log-sum-exp, apply R_v^T with the Walsh-Hadamard butterflies, bf16 out).
 #include <cuda_runtime.h>
 
+#include "tq_chain.cuh"
 #include "tq_dev.cuh"
 #include "tq_encode_vec.cuh"
 
@@ -39,6 +40,7 @@ __global__ void __launch_bounds__(128) prep_kernel(PrepArgs a) {
     __shared__ float wbuf[4][D <= 256 ? D : 4];          // dense rotation only (d <= 256)
     const int lane = threadIdx.x & 31, wl = threadIdx.x >> 5;
     const int64_t row = int64_t(blockIdx.x) * 4 + wl;
+    let_next_in();
     if (row >= a.rows) return;
     float x[E];
     if (a.in_f32) load_vec<D>(reinterpret_cast<const float *>(a.Q) + row * D, lane, x);
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(256) prep_proj128_kernel(PrepArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r0 = int64_t(blockIdx.x) * kPQRows;
     const int j0 = int(blockIdx.y) * JN;
+    let_next_in();
     for (int i = tid; i < JN * 64; i += 256) {  // S[j][k] bf16 pairs -> sT[k][j]
         const int j = j0 + (i >> 6), k2 = (i & 63) * 2;
         const uint32_t pr = *reinterpret_cast<const uint32_t *>(a.kp.S + size_t(j) * 128 + k2);
@@ -673,6 +676,11 @@ int run_attention(const tq_params *kp, const tq_params *vp, const Layout &L, con
             const int e = launch_qproj(pa.qr, rows, D, kp->dev.S, pa.w, st);
             if (e != cudaSuccess) return e;
         }
+    }
+
+    if (s.rows) {
+        const int e = launch_cross_rows(*s.rows, st);
+        if (e != cudaSuccess) return e;
     }
 
     int fast;

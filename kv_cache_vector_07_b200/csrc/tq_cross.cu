@@ -13,22 +13,16 @@
 // bytes alone are 7.
 #include <cuda_runtime.h>
 
+#include "tq_chain.cuh"
 #include "tq_dev.cuh"
 
 namespace tq {
 namespace {
 
-struct RowsArgs {
-    const int32_t *cu_q, *table, *kv_lens;
-    int B, row0, n_rows, max_q, bt_stride, max_kv_len, P, width;
-    int32_t *row_len;        // [n_rows], -1: the row belongs to no run
-    int32_t *row_table;      // [n_rows][width]
-    uint32_t *status;
-};
-
 // One warp per query row of row0 .. row0 + n_rows - 1: its sequence (the last b with cu_q[b] <= row), that
-// sequence's length and its table row.
-__global__ void __launch_bounds__(128) cross_rows_kernel(RowsArgs a) {
+// sequence's length and its table row.  Runs beside the queries' preparation,
+// which it has nothing to do with (4 of 66 us for 32 rows, when it ran first).
+__global__ void __launch_bounds__(128) cross_rows_kernel(CrossRows a) {
     const int lane = threadIdx.x & 31;
     const int at = int(blockIdx.x) * 4 + (threadIdx.x >> 5), row = a.row0 + at;
     if (at >= a.n_rows) return;
@@ -48,6 +42,7 @@ __global__ void __launch_bounds__(128) cross_rows_kernel(RowsArgs a) {
     const int pages = len > 0 ? (len + a.P - 1) / a.P : 0;
     for (int j = lane; j < pages; j += 32)
         a.row_table[int64_t(at) * a.width + j] = a.table[int64_t(lo) * a.bt_stride + j];
+    wait_for_last();         // what comes behind may read what the kernel before wrote
 }
 
 // The queries are taken some at a time, so that the workspace (prepared
@@ -84,6 +79,10 @@ size_t cross_ws_bytes(const Layout &L, const CrossShape &s) {
     return tc > rows ? tc : rows;
 }
 
+int launch_cross_rows(const CrossRows &a, void *stream) {
+    return launch_next(cross_rows_kernel, dim3(unsigned((a.n_rows + 3) / 4)), 128, 0, static_cast<cudaStream_t>(stream), a);
+}
+
 int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, const void *Q, const CrossShape &s,
                  const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream) {
     if (cross_tc_covers(L, kp->dev.rot || vp->dev.rot, s))
@@ -91,7 +90,7 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
     const int n = queries_at_once(s);
     AttnShape r = rows_shape(L, s, n);
     const size_t inner = up256(attn_ws_bytes(L, r));
-    RowsArgs a;
+    CrossRows a;
     a.cu_q = s.cu_q;
     a.table = s.block_table;
     a.kv_lens = s.kv_lens;
@@ -106,10 +105,10 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
     a.status = reinterpret_cast<uint32_t *>(ws);
     r.seq_lens = a.row_len;
     r.block_table = a.row_table;
+    r.rows = &a;
     for (int q0 = 0; q0 < s.total_q; q0 += n) {
         a.row0 = q0;
         a.n_rows = r.n_seq = s.total_q - q0 < n ? s.total_q - q0 : n;
-        cross_rows_kernel<<<unsigned((a.n_rows + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
         const int64_t at = int64_t(q0) * s.Hq;
         const int e = launch_attention(kp, vp, L, static_cast<const uint16_t *>(Q) + at * L.d, r, cache, num_blocks,
                                        static_cast<uint16_t *>(out) + at * L.d, lse ? lse + at : nullptr, nullptr, 0, ws,

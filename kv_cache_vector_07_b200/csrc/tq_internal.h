@@ -175,6 +175,17 @@ int launch_encode128(const tq_params *kp, const tq_params *vp, const Layout &L, 
                      int64_t n_tokens, const int32_t *slots, uint8_t *cache, int64_t num_blocks, uint8_t *ws,
                      void *stream);
 
+// Cross attention by rows: every query row row0 .. n_rows - 1 of Q as a decode row.
+struct CrossRows {
+    const int32_t *cu_q, *table, *kv_lens;
+    int B, row0, n_rows, max_q, bt_stride, max_kv_len, P, width;
+    int32_t *row_len;        // [n_rows], -1: the row belongs to no run
+    int32_t *row_table;      // [n_rows][width]
+    uint32_t *status;
+};
+// Fills row_len and row_table, beside the kernel launched before it.
+int launch_cross_rows(const CrossRows &rows, void *stream);
+
 struct AttnShape {
     int n_seq;            // decode: batch; prefill: chunk length C
     int Hq;
@@ -186,6 +197,7 @@ struct AttnShape {
     int max_len;          // longest visible length
     int is_decode;        // 1: decode (per-sequence lengths), 0: prefill chunk
     int cross;            // 1: rows of cross attention (those of a negative length are not written)
+    const CrossRows *rows;     // cross: what fills seq_lens and block_table
 };
 // New tokens of a fused decode step (one per sequence): bf16 K and V
 // [B][H][d], their slots, and the cache they are written into.
