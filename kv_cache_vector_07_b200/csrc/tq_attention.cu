@@ -483,6 +483,7 @@ template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(CombineArgs a) {
     constexpr int E = WarpVec<D>::E;
     __shared__ float wbuf[4][D <= 256 ? D : 4];          // dense rotation only (d <= 256)
+    wait_for_last();
     const int lane = threadIdx.x & 31;
     const int64_t r = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (r >= int64_t(a.n_groups) * a.G) return;
@@ -734,6 +735,7 @@ int run_attention(const tq_params *kp, const tq_params *vp, const Layout &L, con
     c.row_lens = s.cross ? s.seq_lens : nullptr;
     c.Q = static_cast<const __nv_bfloat16 *>(Q);
     const int64_t crow = int64_t(p.n_groups) * p.G;
+    if (s.rows) return launch_next(combine_kernel<D>, dim3(unsigned((crow + 3) / 4)), 128, 0, st, c);
     combine_kernel<D><<<unsigned((crow + 3) / 4), 128, 0, st>>>(c);
     return cudaGetLastError();
 }

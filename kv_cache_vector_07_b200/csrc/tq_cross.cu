@@ -23,6 +23,7 @@ namespace {
 // sequence's length and its table row.  Runs beside the queries' preparation,
 // which it has nothing to do with (4 of 66 us for 32 rows, when it ran first).
 __global__ void __launch_bounds__(128) cross_rows_kernel(CrossRows a) {
+    let_next_in();
     const int lane = threadIdx.x & 31;
     const int at = int(blockIdx.x) * 4 + (threadIdx.x >> 5), row = a.row0 + at;
     if (at >= a.n_rows) return;

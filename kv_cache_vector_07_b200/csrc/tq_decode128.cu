@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include "tc05.cuh"
+#include "tq_chain.cuh"
 #include "tq_dev.cuh"
 
 namespace tq {
@@ -92,6 +93,7 @@ struct Dec128Args {
     float *logits;
     int64_t logits_stride;
     uint32_t *status;
+    bool chained;                  // launched behind a kernel of the same call (launch_next)
     uint32_t stall_polls;          // testing aid: > 0 makes every block first wait
                                    // this many polls on a barrier nothing completes
 };
@@ -203,6 +205,8 @@ __global__ void __launch_bounds__(128) dec128_kernel(Dec128Args a) {
     int *pvalid = reinterpret_cast<int *>(never + 1);
     volatile int *abort_flag = pvalid + kNS;
 
+    wait_for_last();
+    let_next_in();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int grp = blockIdx.x, split = blockIdx.y;
@@ -985,7 +989,9 @@ int run_dec(const Dec128Args &a, int n_groups, cudaStream_t st) {
     auto kern = dec128_kernel<KB, VB, NT, FR, PL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kern<<<dim3(unsigned(n_groups), unsigned(a.n_splits)), 128, smem, st>>>(a);
+    const dim3 grid{unsigned(n_groups), unsigned(a.n_splits)};
+    if (a.chained) return launch_next(kern, grid, 128, smem, st, a);
+    kern<<<grid, 128, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -1066,6 +1072,7 @@ int launch_dec128(const tq_params *kp, const tq_params *vp, const Layout &L, con
     a.logits_stride = logits_stride;
     a.status = status;
     a.stall_polls = take_decode_stall();
+    a.chained = s.rows != nullptr;
     const bool two = G > 4;
     if (polar)
         return two ? run_dec<4, 4, 2, false, true>(a, n_groups, st) : run_dec<4, 4, 1, false, true>(a, n_groups, st);
