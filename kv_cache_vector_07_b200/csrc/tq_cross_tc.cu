@@ -581,7 +581,8 @@ struct AttendArgs {
     int n_splits, split_tiles;
     __nv_bfloat16 *out;
     float *lse;
-    float *part_o, *part_ml;               // [split][pair][max_q G][D], [..][2]
+    int x;                                 // blocks of 256 query rows of the longest run
+    float *part_o, *part_ml;               // [split][pair][x][2 query tiles], see part_tile
     uint32_t *status;
 };
 
@@ -593,9 +594,10 @@ __device__ __forceinline__ int run_of(const AttendArgs &a, int b, int *first, bo
     return q0 >= 0 && q1 > q0 ? min(q1 - q0, a.max_q) : 0;
 }
 
-// Where the partial result of a pair's row i (position x heads + head) lies.
-__device__ __forceinline__ int64_t part_row(const AttendArgs &a, int split, int pl, int64_t i) {
-    return (int64_t(split) * gridDim.y + pl) * (int64_t(a.max_q) * a.G) + i;
+// The partial results of a query tile lie together: [row][2] (maximum, sum) and
+// [D / 4][row][4], so that the threads of a warp, a row each, write side by side.
+__device__ __forceinline__ int64_t part_tile(const AttendArgs &a, int split, int pl, int x, int tt) {
+    return (((int64_t(split) * gridDim.y + pl) * a.x) + x) * 2 + tt;
 }
 
 // Unnormalised Walsh-Hadamard transform of a vector in registers.
@@ -663,13 +665,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     const int qpos = pos0 + tt * a.PT + r / a.G;
     const bool row_ok = tid < 256 && r < a.PT * a.G && qpos < nq;
     const int64_t row = (int64_t(q0) + qpos) * a.Hq + h * a.G + r % a.G;
-    const int64_t prow = part_row(a, split, pl, int64_t(qpos) * a.G + r % a.G);
+    const int64_t part = part_tile(a, split, pl, blockIdx.x, tt) * kTile;
 
     if (n <= 0) {                                         // no key of this split
         if (!row_ok) return;
         if (a.n_splits > 1) {
-            a.part_ml[prow * 2] = -INFINITY;
-            a.part_ml[prow * 2 + 1] = 0.f;
+            *reinterpret_cast<float2 *>(a.part_ml + (part + r) * 2) = make_float2(-INFINITY, 0.f);
         } else {
             for (int i = 0; i < D / 8; ++i)
                 reinterpret_cast<uint4 *>(a.out + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -993,11 +994,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) o[i] = make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
         if (row_ok && a.n_splits > 1) {
-            float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D);
+            float4 *dst = reinterpret_cast<float4 *>(a.part_o + part * D) + r;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
-            a.part_ml[prow * 2] = m;
-            a.part_ml[prow * 2 + 1] = l;
+            for (int i = 0; i < D / 4; ++i) dst[i * kTile] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+            *reinterpret_cast<float2 *>(a.part_ml + (part + r) * 2) = make_float2(m, l);
         } else if (row_ok) {
             fwht_regs<D>(o);
             const float inv = (l != l || l > 0.f ? 1.f / l : 0.f) * rsqrtf(float(D));
@@ -1026,66 +1026,87 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
     if (timeout) atomicOr(a.status, TQ_DEV_WAIT_TIMEOUT);
 }
 
-// Merges the splits of a row: one warp a row.
+// Merges the splits: eight threads a row (an eighth of its coordinates each),
+// four rows a warp, so that a warp's loads are 64 bytes side by side, those of
+// four splits on their way at once.
 template <int D>
 __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ AttendArgs a) {
-    constexpr int E = D / 32;
+    constexpr int Q = D / 8;                              // coordinates of a thread
     wait_for_last();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, eighth = lane >> 2;
+    const int x = int(blockIdx.x) >> 4, tt = (int(blockIdx.x) >> 3) & 1;
+    const int r = (int(blockIdx.x) & 7) * 16 + (threadIdx.x >> 5) * 4 + (lane & 3);
     const int pl = int(blockIdx.y), pair = a.pair0 + pl, b = pair / a.H, h = pair - b * a.H;
-    const int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5);
     int q0;
     bool cut;
-    const int nq = run_of(a, b, &q0, &cut);
-    if (i >= nq * a.G) return;
-    const int64_t row = (int64_t(q0) + i / a.G) * a.Hq + h * a.G + i % a.G;
-    const int64_t first = part_row(a, 0, pl, i), step = part_row(a, 1, pl, i) - first;
-    // lane s holds split s of a round of 32: the weights of all are there before
-    // the first partial is asked for, and four partials are on their way at once
+    const int nq = run_of(a, b, &q0, &cut), qpos = (2 * x + tt) * a.PT + r / a.G;
+    const bool ok = r < a.PT * a.G && qpos < nq;
+    if (!__any_sync(kFull, ok)) return;
+    const int64_t first = part_tile(a, 0, pl, x, tt) * kTile, step = part_tile(a, 1, pl, x, tt) * kTile - first;
+    auto ml = [&](int s) {                                // a split without keys (or another run's row): sum 0
+        return ok ? *reinterpret_cast<const float2 *>(a.part_ml + (first + s * step + r) * 2) : make_float2(-INFINITY, 0.f);
+    };
     float M = -INFINITY;
-    for (int s = lane; s < a.n_splits; s += 32)
-        if (a.part_ml[(s * step + first) * 2 + 1] != 0.f) M = fmaxf(M, a.part_ml[(s * step + first) * 2]);
-    M = warp_max(M);
-    float l = 0.f, o[E];
+#pragma unroll 8
+    for (int s = 0; s < a.n_splits; ++s) {
+        const float2 w = ml(s);
+        if (w.y != 0.f) M = fmaxf(M, w.x);
+    }
+    float l = 0.f;
+    float2 o[Q / 2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int s0 = 0; s0 < a.n_splits; s0 += 32) {
-        const int s = s0 + lane, n = min(32, a.n_splits - s0);
-        float f = 0.f;                                    // 0: no key there
-        if (s < a.n_splits) {
-            const float ls = a.part_ml[(s * step + first) * 2 + 1];
-            if (ls != 0.f) {
-                f = exp2f(a.part_ml[(s * step + first) * 2] - M);
-                l = fmaf(ls, f, l);
-            }
+    for (int i = 0; i < Q / 2; ++i) o[i] = make_float2(0.f, 0.f);
+    for (int s0 = 0; s0 < a.n_splits; s0 += 4) {
+        float f[4];
+        float4 v[4][Q / 4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 w = s0 + k < a.n_splits ? ml(s0 + k) : make_float2(-INFINITY, 0.f);
+            f[k] = w.y != 0.f ? exp2f(w.x - M) : 0.f;
+            l = fmaf(w.y, f[k], l);
         }
-        for (int i = 0; i < n; i += 4) {
-            float v[4][E], w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                w[k] = __shfl_sync(kFull, f, (i + k) & 31);
-                if (i + k >= n) w[k] = 0.f;
-                if (w[k] != 0.f) {
-                    load_vec<D>(a.part_o + ((s0 + i + k) * step + first) * D, lane, v[k]);
-                } else {
+        for (int k = 0; k < 4; ++k) {
+            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (first + (s0 + k) * step) * D) +
+                                eighth * (Q / 4) * kTile + r;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-                }
+            for (int i = 0; i < Q / 4; ++i) v[k][i] = f[k] != 0.f ? src[i * kTile] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < Q / 4; ++i) {
+                o[2 * i] = fma2(make_float2(v[k][i].x, v[k][i].y), make_float2(f[k], f[k]), o[2 * i]);
+                o[2 * i + 1] = fma2(make_float2(v[k][i].z, v[k][i].w), make_float2(f[k], f[k]), o[2 * i + 1]);
             }
+    }
+    // the transform's last three stages go across the row's threads
+    fwht_regs<Q>(o);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+    for (int bit = 4; bit <= 16; bit <<= 1) {
+        const float sg = lane & bit ? -1.f : 1.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(v[k][e], w[k], o[e]);
+        for (int i = 0; i < Q / 2; ++i) {
+            const float2 y = make_float2(__shfl_xor_sync(kFull, o[i].x, bit), __shfl_xor_sync(kFull, o[i].y, bit));
+            o[i] = fma2(o[i], make_float2(sg, sg), y);
         }
     }
-    l = warp_sum(l);
-    fwht_warp<D>(o, lane);
-    float sg[E];
-    load_vec<D>(a.vsigns, lane, sg);
+    if (!ok) return;
+    const int64_t row = (int64_t(q0) + qpos) * a.Hq + h * a.G + r % a.G;
     const float inv = (l != l || l > 0.f ? 1.f / l : 0.f) * rsqrtf(float(D));
+    sign_regs<Q>(o, a.vsigns + eighth * Q);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D + eighth * Q);
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv * sg[e]);
-    if (a.lse && lane == 0) a.lse[row] = l != l ? l : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    for (int c = 0; c < Q / 8; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[4 * c + e].x * inv, o[4 * c + e].y * inv);
+            w[e] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (a.lse && eighth == 0) a.lse[row] = l != l ? l : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Sizes of a call: the workspace holds the operand tiles of as many (sequence,
@@ -1109,12 +1130,20 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     if (fit > 65535) fit = 65535;
     p.round = int(fit < size_t(p.pairs) ? fit : size_t(p.pairs));
     p.x = (s.max_q + 2 * PT - 1) / (2 * PT);
-    // fewer than three waves of blocks: the key axis is split, into pieces of at
-    // least eight tiles (8 runs of 77 x 32 heads over up to 4,096 states: 83 us
-    // unsplit, 65 with four pieces and 11 to merge them)
-    const int64_t blocks = int64_t(p.x) * p.round;
-    int sp = int((3 * 148 + blocks - 1) / (blocks < 1 ? 1 : blocks));
-    if (sp > p.n_tiles / 8) sp = p.n_tiles / 8;
+    // The key axis is split where blocks are few: into pieces of four tiles or
+    // more while the pieces fill the SMs but once, beyond that of eight or more
+    // and up to two and a half blocks an SM (they run one after another, which
+    // evens out runs and sequences of different lengths; every partial result
+    // costs a write and a read).  Keys of 2 bits with a sketch, values of 4, 32
+    // heads, against three waves of eight tiles everywhere: one run of 300 over
+    // 1,500 states 41 us against 47, 8 of up to 77 over up to 4,096 94 against
+    // 104, 2 of 512 over 4,096 125 against 158, but 2 of up to 77 over up to
+    // 32,768 207 against 201.
+    const int64_t blocks = int64_t(p.x) * p.round < 1 ? 1 : int64_t(p.x) * p.round;
+    const int64_t once = 148 / blocks, more = 148 * 5 / 2 / blocks;
+    int sp = int(once < p.n_tiles / 4 ? once : p.n_tiles / 4);
+    const int sp8 = int(more < p.n_tiles / 8 ? more : p.n_tiles / 8);
+    if (sp < sp8) sp = sp8;
     if (sp < 1) sp = 1;
     p.split_tiles = (p.n_tiles + sp - 1) / sp;
     p.n_splits = (p.n_tiles + p.split_tiles - 1) / p.split_tiles;
@@ -1123,7 +1152,7 @@ TcPlan tc_plan(const Layout &L, const CrossShape &s) {
     p.off_order = take(size_t(p.round) * 4);
     p.off_meta = take(size_t(p.round) * p.n_tiles * sizeof(TileMeta));
     p.off_img = take(size_t(p.round) * pair_bytes);
-    const size_t rows = size_t(p.round) * size_t(s.max_q) * G * p.n_splits;
+    const size_t rows = size_t(p.round) * size_t(p.x) * 2 * kTile * p.n_splits;
     p.off_po = take(p.n_splits > 1 ? rows * L.d * 4 : 0);
     p.off_pml = take(p.n_splits > 1 ? rows * 8 : 0);
     p.total = off;
@@ -1182,6 +1211,7 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
     a.meta = x.meta;
     a.ksigns = kp->dev.signs;
     a.vsigns = vp->dev.signs;
+    a.x = p.x;
     a.n_splits = p.n_splits;
     a.split_tiles = p.split_tiles;
     a.out = static_cast<__nv_bfloat16 *>(out);
@@ -1198,8 +1228,7 @@ int run_tc(const tq_params *kp, const tq_params *vp, const Layout &L, const void
         e = launch_next(cross_attend_kernel<D>, dim3(unsigned(p.x), unsigned(np), unsigned(p.n_splits)), kAttendThreads,
                         attend_smem<D>(), st, a);
         if (e == cudaSuccess && p.n_splits > 1)
-            e = launch_next(cross_merge_kernel<D>, dim3(unsigned((int64_t(s.max_q) * a.G + 3) / 4), unsigned(np)), 128, 0,
-                            st, a);
+            e = launch_next(cross_merge_kernel<D>, dim3(unsigned(p.x) * 16u, unsigned(np)), 128, 0, st, a);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
