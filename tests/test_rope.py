@@ -149,6 +149,30 @@ def test_empty_zero_and_non_finite_vectors():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("style", ["half", "pairs"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rot", [(8, 8), (16, 8), (32, 32), (64, 32), (64, 48), (128, 128), (256, 192), (256, 0)])
+def test_few_heads(d, rot, dtype, style):
+    """As many heads as a warp takes at once, one less, one more; either side alone, a norm on one side only."""
+    most = 2 * 256 // d
+    n = 37
+    pos = torch.arange(n, device=DEV, dtype=torch.int32) * 1001 - 500
+    inv = frequencies(rot // 2)
+    rd = tqkv.rope_desc(d, rot, tqkv.TQ_ROPE_HALF if style == "half" else tqkv.TQ_ROPE_PAIRS)
+    for heads, wt in ((most - 1, dtype), (most, torch.float32), (most + 1, torch.bfloat16)):
+        hk = max(1, heads // 3)
+        hq = max(1, heads - hk)
+        q, k, w = inputs(n, hq, hk, d, dtype, heads)
+        w = [x.to(wt) for x in w]
+        for qw, kw in ((w[0], w[1]), (None, w[1]), (w[0], None)):
+            gq, gk = tqkv.qk_norm_rope(rd, q, k, pos, inv, qw, kw)
+            check(rd, gq, q, qw, pos, inv)
+            check(rd, gk, k, kw, pos, inv)
+        check(rd, tqkv.qk_norm_rope(rd, q, None, pos, inv, w[0])[0], q, w[0], pos, inv)
+        check(rd, tqkv.qk_norm_rope(rd, None, k, pos, inv, None, w[1])[1], k, w[1], pos, inv)
+
+
+@pytest.mark.gpu
 def test_results_it_makes_belong_to_its_stream():
     """Room that the current stream still writes to is not given to a call on another one."""
     n, d = 4096, 128
