@@ -240,9 +240,14 @@ template <int D>
 constexpr size_t expand_smem() { return size_t(D) * D * 2 + 2 * image_bytes(D) + 1024; }
 
 // Power of two that brings mx to [2^(top - 1), 2^top); *e: value = stored * 2^e.
+// Zeros get an exponent below any other tile's (the smallest norm, 2^-24, times
+// the smallest largest level, 2^-4: -42): a tile without values then never sets
+// the reference that the other tiles' weights are relative to.
+constexpr int kZeroExponent = -45;
 __device__ __forceinline__ float scale_to(float mx, int top, int *e) {
     int ex = top;
-    if (mx > 0.f && mx < INFINITY) frexpf(mx, &ex);
+    if (mx == 0.f) ex = top + kZeroExponent;
+    else if (mx < INFINITY) frexpf(mx, &ex);
     *e = ex - top;
     return ldexpf(1.f, top - ex);
 }
@@ -598,6 +603,14 @@ __device__ __forceinline__ int run_of(const AttendArgs &a, int b, int *first, bo
 // [D / 4][row][4], so that the threads of a warp, a row each, write side by side.
 __device__ __forceinline__ int64_t part_tile(const AttendArgs &a, int split, int pl, int x, int tt) {
     return (((int64_t(split) * gridDim.y + pl) * a.x) + x) * 2 + tt;
+}
+
+// (m + log2 l) ln 2.  l may be 2^50 and m as far below zero (tiles of zeros), so
+// l's exponent is taken to m before the rest, which is in [-1, 0), is added.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    int e;
+    const float f = frexpf(l, &e);
+    return ((m + float(e)) + log2f(f)) * 0.6931471805599453f;
 }
 
 // Unnormalised Walsh-Hadamard transform of a vector in registers.
@@ -1013,7 +1026,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
                 }
                 dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (a.lse) a.lse[row] = l != l ? l : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (a.lse) a.lse[row] = l != l ? l : l > 0.f ? lse_of(m, l) : -INFINITY;
         }
     }
     }
@@ -1106,7 +1119,7 @@ __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant_
         }
         dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (a.lse && eighth == 0) a.lse[row] = l != l ? l : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (a.lse && eighth == 0) a.lse[row] = l != l ? l : l > 0.f ? lse_of(M, l) : -INFINITY;
 }
 
 // Sizes of a call: the workspace holds the operand tiles of as many (sequence,

@@ -1,0 +1,73 @@
+"""tq_cross_attn where the sizes of states and values differ: zero states among others.
+
+Formula, tolerances and their derivation: test_cross.py.
+"""
+import functools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_vector_07_b200 import tqkv
+from test_cross import CODECS, DEV, Call, Codec
+
+pytestmark = pytest.mark.gpu
+
+
+@functools.lru_cache(maxsize=None)
+def codec_of(name, H):
+    return Codec(*CODECS[name], H=H)
+
+
+class Made(Call):
+    """Every sequence's states around one logit: key t of a sequence gives about -below bits, or
+    0 where it is a zero state (key and value); values of the given norms."""
+
+    def __init__(self, cd, qlens, kvlens, G, zero, below, norms, seed=0):
+        super().__init__(cd, qlens, kvlens, G, seed=seed)
+        d, H, g = cd.d, cd.H, torch.Generator().manual_seed(seed + 10)
+        u = torch.randn(d, generator=g, dtype=torch.float64)
+        u /= u.norm()
+        for slots in self.slots:
+            n = len(slots)
+            K = 0.3 * torch.randn((n, H, d), generator=g, dtype=torch.float64) - below * math.log(2) * u
+            V = torch.randn((n, H, d), generator=g, dtype=torch.float64)
+            V *= (torch.as_tensor(norms(np.arange(n)), dtype=torch.float64)[:, None, None] / V.norm(dim=2, keepdim=True))
+            z = torch.as_tensor(zero(np.arange(n), n))
+            K[z], V[z] = 0, 0
+            tqkv.encode(cd.kp, cd.vp, cd.desc, *(x.to(torch.bfloat16).to(DEV).contiguous() for x in (K, V)),
+                        torch.from_numpy(slots).to(DEV), self.cache)
+        noise = torch.randn(self.Q.shape, generator=g, dtype=torch.float64)
+        self.Q.copy_(math.sqrt(d) * u + 0.3 * noise)
+
+
+def constant(norm):
+    return lambda t: np.full(len(t), norm)
+
+
+ZEROS = {
+    "start": lambda t, n: t < 128, "two tiles": lambda t, n: t < 256, "middle": lambda t, n: (t >= 256) & (t < 512),
+    "end": lambda t, n: t >= n // 128 * 128 - 128,
+}
+
+
+@pytest.mark.parametrize("codec,qlens", [("k5v4", [70]), ("k5v4", [1]), ("d64", [70]), ("d64", [1])])
+@pytest.mark.parametrize("length", [880, 1024])                       # seven tiles in one piece, eight in two
+@pytest.mark.parametrize("where", list(ZEROS))
+def test_zero_tiles(codec, qlens, length, where):
+    for norm in (11.0, 0.1, 0.003):
+        for below in (0, 4, 8):
+            c = Made(codec_of(codec, 1), qlens, [length], 4, ZEROS[where], below, constant(norm))
+            out, lse, flags = c.run()
+            assert flags == 0
+            c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64"])
+def test_nothing_but_zero_states(codec):
+    for qlens in ([70, 3], [1, 1]):
+        c = Made(codec_of(codec, 2), qlens, [1024, 77], 2, lambda t, n: t >= 0, 0, constant(1.0))
+        out, lse, flags = c.run()
+        assert flags == 0 and (out[:sum(qlens)] == 0).all()
+        c.check(out, lse)
