@@ -242,12 +242,14 @@ constexpr size_t expand_smem() { return size_t(D) * D * 2 + 2 * image_bytes(D) +
 // Power of two that brings mx to [2^(top - 1), 2^top); *e: value = stored * 2^e.
 // Zeros get an exponent below any other tile's (the smallest norm, 2^-24, times
 // the smallest largest level, 2^-4: -42): a tile without values then never sets
-// the reference that the other tiles' weights are relative to.
+// the reference that the other tiles' weights are relative to.  The factor ends
+// at 2^127: what is smaller than 2^(top - 128) (tiny queries) stays below 2^(top - 1).
 constexpr int kZeroExponent = -45;
 __device__ __forceinline__ float scale_to(float mx, int top, int *e) {
     int ex = top;
     if (mx == 0.f) ex = top + kZeroExponent;
     else if (mx < INFINITY) frexpf(mx, &ex);
+    ex = max(ex, top - 127);
     *e = ex - top;
     return ldexpf(1.f, top - ex);
 }

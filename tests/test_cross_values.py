@@ -1,4 +1,5 @@
-"""tq_cross_attn where the sizes of states and values differ: zero states among others.
+"""tq_cross_attn where the sizes of states, values and queries differ: zero states,
+queries near the end of bf16's range.
 
 Formula, tolerances and their derivation: test_cross.py.
 """
@@ -71,3 +72,21 @@ def test_nothing_but_zero_states(codec):
         out, lse, flags = c.run()
         assert flags == 0 and (out[:sum(qlens)] == 0).all()
         c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64"])
+@pytest.mark.parametrize("qlens", [[3, 1], [70, 9]])
+def test_tiny_queries(codec, qlens):
+    """Coordinates down to bf16's smallest: the mean of the values, and no other row changes."""
+    c = Call(codec_of(codec, 2), qlens, [1100, 300], 2)
+    ref, rl, _ = c.run()
+    n = sum(qlens)
+    tiny = {(0, 0): 2.0 ** -116, (0, 1): 1e-37, (1, 3): 2.0 ** -133, (n - 1, 2): 1e-36, (n - 1, 0): 0.0}
+    keep = torch.ones(c.Q.shape[:2], dtype=torch.bool, device=DEV)
+    for (row, head), x in tiny.items():
+        c.Q[row, head] = (torch.randn(c.cd.d, generator=torch.Generator().manual_seed(row)).sign() * x).to(torch.bfloat16).to(DEV)
+        keep[row, head] = False
+    c.Q[0, 1, 5:] = 0                                                 # few coordinates that are not zero
+    out, lse, flags = c.run()
+    assert flags == 0 and torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rl[keep])
+    c.check(out, lse)
