@@ -18,11 +18,14 @@
 //            online softmax between them, a thread per row.
 //
 // Queries are rotated and scaled to fp16 as they are staged (the same range),
-// softmax weights are fp16, all sums fp32: each operand is off by at most
-// 2^-11 of itself, eight times finer than the bf16 result.  The tile scales
-// ride along for nothing: the key's on the factor that turns S into a
-// logarithm, the value's (2^e) on its offset, P' = 2^(l + e - m) with m the
-// running maximum of l + e, while the sum takes P' 2^-e.
+// softmax weights are fp16, all sums fp32: queries and states are off by at
+// most 2^-11 of themselves, eight times finer than the bf16 result.  The tile
+// scales ride along for nothing: the key's on the factor that turns S into a
+// logarithm, the value's (2^e) on its offset, P' = 2^(l + e - m), while the sum
+// takes P' 2^-e.  The reference m follows l + e at a distance that keeps the
+// strongest weight of every tile between 2^-9 and 2^15: a weight is off by at
+// most 2^-11 of itself or 2^-25, the smallest step of fp16, which is 2^-16 of
+// its tile's strongest at worst and 2^-32 of the one that set m.
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -952,12 +955,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             const float c2 = fmaxf(rowc * sc.x, 1e-37f);
             const float top = fmaf(mx, c2, sc.y);
-            // the reference moves only when it is beaten by 2^8: weights stay
-            // within fp16, and O is rescaled a few times a row, not every tile
-            const bool move = top > m + 8.f;
-            const float alpha = move ? exp2f(m - top) : 1.f;
+            // Set to 2^7 below the strongest weight, the reference moves only
+            // when a tile's strongest leaves [2^-9, 2^15], so O is rescaled a
+            // few times a row, not every tile.  It moves down, too: where one
+            // strong key has a small value, the result is made of the others'
+            // weights.  O and the sum, fp32, grow by 2^30 at most a time while
+            // the sum is below 2^60, and stay below 2^106.
+            const float d = top - m;
+            const bool move = d > 15.f || (d < -9.f && d > -1e30f && l < 0x1p60f);
+            const float ref = fmaxf(top - 7.f, m - 30.f);
+            const float alpha = move ? exp2f(m - ref) : 1.f;
             if (move) {
-                m = top;
+                m = ref;
                 l *= alpha;
             }
             if (j > 0 && __any_sync(kFull, move)) {

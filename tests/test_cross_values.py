@@ -1,7 +1,9 @@
-"""tq_cross_attn where the sizes of states, values and queries differ: zero states,
-queries near the end of bf16's range.
+"""tq_cross_attn where the sizes of states, values and queries differ: zero states, value norms
+that change from tile to tile, strong keys without a value, queries near the end of bf16's range.
 
-Formula, tolerances and their derivation: test_cross.py.
+Formula, tolerances and their derivation: test_cross.py.  The roundings counted there are
+relative to a weight; what a kernel may lose of weights far below their neighbours' is not
+counted, so the cases hold it to a share of the result that the tolerances leave open.
 """
 import functools
 import math
@@ -10,7 +12,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cache_vector_07_b200 import tqkv
+from kv_cache_vector_07_b200 import synth, tqkv
 from test_cross import CODECS, DEV, Call, Codec
 
 pytestmark = pytest.mark.gpu
@@ -66,12 +68,62 @@ def test_zero_tiles(codec, qlens, length, where):
 
 
 @pytest.mark.parametrize("codec", ["k5v4", "d64"])
+@pytest.mark.parametrize("length", [700, 4096])
+@pytest.mark.parametrize("below", [16, 30, 45])
+def test_zero_tiles_far_above_the_rest(codec, length, below):
+    """Tiles of zero states hold all of the sum and none of the result."""
+    for where in ("start", "middle"):
+        c = Made(codec_of(codec, 1), [70, 7], [length, 640], 2, ZEROS[where], below, constant(0.02))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64"])
 def test_nothing_but_zero_states(codec):
     for qlens in ([70, 3], [1, 1]):
         c = Made(codec_of(codec, 2), qlens, [1024, 77], 2, lambda t, n: t >= 0, 0, constant(1.0))
         out, lse, flags = c.run()
         assert flags == 0 and (out[:sum(qlens)] == 0).all()
         c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64"])
+@pytest.mark.parametrize("at", [0, 2000])
+@pytest.mark.parametrize("below", [16, 20, 22, 24])
+def test_one_strong_key_without_a_value(codec, at, below):
+    """The result is made of weights below 2^-below of the largest alone."""
+    for length in (880, 4096):
+        c = Made(codec_of(codec, 1), [70], [length], 4, lambda t, n: t == at % n, below, constant(1.0))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec,qlens", [("k5v4", [70]), ("k5v4", [2]), ("d64", [70]), ("d64k8", [90])])
+@pytest.mark.parametrize("length", [880, 4096])
+def test_value_norms_that_differ_between_tiles(codec, qlens, length):
+    steps = np.array([0, -8, 8, 3, -12, 6, -3])
+    c = Made(codec_of(codec, 1), qlens, [length], 4, lambda t, n: t < 0, 0, lambda t: 2.0 ** steps[t // 128 % 7])
+    out, lse, flags = c.run()
+    assert flags == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64"])
+@pytest.mark.parametrize("length", [880, 4096])
+def test_loud_values_that_nothing_looks_at(codec, length):
+    """Every other tile ends with a value 2^12 times the others' size whose weight is nothing."""
+    cd = codec_of(codec, 1)
+    c = Made(cd, [70], [length], 2, lambda t, n: t < 0, 0, lambda t: np.where(t % 256 == 127, 40.0, 0.01))
+    loud = torch.from_numpy(c.slots[0][127::256].copy()).to(DEV)
+    q = c.Q.double().mean((0, 1))
+    K = (q / q.norm() * -40.0).to(torch.bfloat16).expand(len(loud), 1, cd.d).contiguous()
+    V = synth.normal((len(loud), 1, cd.d), seed=77, device=DEV) * 4.0
+    tqkv.encode(cd.kp, cd.vp, cd.desc, K, V, loud, c.cache)
+    out, lse, flags = c.run()
+    assert flags == 0
+    c.check(out, lse)
 
 
 @pytest.mark.parametrize("codec", ["k5v4", "d64"])
