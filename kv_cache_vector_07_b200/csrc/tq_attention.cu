@@ -587,7 +587,8 @@ Plan make_plan(const Layout &L, const AttnShape &s) {
     int sms = 148;
     const int maxlen = s.max_len > 0 ? s.max_len : 1;
     const int64_t target = int64_t(sms) * 4;
-    int splits = int((target + p.n_groups - 1) / p.n_groups);
+    const int64_t groups = p.n_groups > 0 ? p.n_groups : 1;      // no query: the size of a call that does nothing
+    int splits = int((target + groups - 1) / groups);
     const int max_splits = (maxlen + kChunk - 1) / kChunk;
     if (splits > max_splits) splits = max_splits;
     if (splits < 1) splits = 1;
@@ -616,7 +617,7 @@ Plan make_plan(const Layout &L, const AttnShape &s) {
             // sequences of very different lengths: pieces of eight pages, up to
             // two waves of them (32 rows over up to 2,048 tokens: 50 us in two
             // pieces a row, 47 in four, 56 in eight)
-            const int64_t fill = p.n_groups > 0 ? 2 * slots / p.n_groups : 1;
+            const int64_t fill = 2 * slots / groups;
             best = max_sp < 1 || fill < 1 ? 1 : int(fill < max_sp ? fill : max_sp);
         }
         split_len = (maxlen + best - 1) / best;

@@ -142,3 +142,14 @@ def test_tiny_queries(codec, qlens):
     out, lse, flags = c.run()
     assert flags == 0 and torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rl[keep])
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64", "d32"])
+def test_no_queries_and_no_sequences(codec):
+    """A step in which nothing is to be read: the call returns, and writes nothing."""
+    c = Call(codec_of(codec, 2), [3, 0], [70, 9], 2)
+    kp, vp, desc, Q, cu, max_q, table, lens, most, cache = c.args
+    assert tqkv.cross_attn(kp, vp, desc, Q[:0], torch.zeros_like(cu), 0, table, lens, most, cache).shape == (0, *Q.shape[1:])
+    assert tqkv.cross_attn(kp, vp, desc, Q[:0], torch.zeros_like(cu), max_q, table, lens, most, cache).numel() == 0
+    assert (tqkv.cross_attn(kp, vp, desc, Q, cu[:1], max_q, table[:0], lens[:0], most, cache) == 0).all()
+    assert (tqkv.cross_attn(kp, vp, desc, Q, torch.zeros_like(cu), max_q, table, lens, most, cache) == 0).all()
