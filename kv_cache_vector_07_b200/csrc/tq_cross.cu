@@ -46,14 +46,6 @@ __global__ void __launch_bounds__(128) cross_rows_kernel(CrossRows a) {
     wait_for_last();         // what comes behind may read what the kernel before wrote
 }
 
-// The queries are taken some at a time, so that the workspace (prepared
-// queries, partial results, table rows) stays within some 100 MB whatever their
-// number: 65,536 rows of a head.
-int queries_at_once(const CrossShape &s) {
-    const int most = 65536 / s.Hq;
-    return s.total_q < most ? s.total_q : most > 1 ? most : 1;
-}
-
 AttnShape rows_shape(const Layout &L, const CrossShape &s, int n) {
     AttnShape r{};
     r.n_seq = n;
@@ -68,13 +60,40 @@ AttnShape rows_shape(const Layout &L, const CrossShape &s, int n) {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The queries are taken some at a time, so that what a round holds (prepared
+// queries, one partial result a row, lengths, a table row for every query) stays
+// within 128 MB whatever the number of queries, their heads and the states'
+// length; a query alone takes what it needs.  65,536 rows of a head at most.  (A
+// round of few rows has its keys split, which adds up to 2,400 x G partial results.)
+struct RowsPlan {
+    int n;                       // queries of a round
+    size_t inner, lens, total;   // workspace of the decode kernels; the rows' lengths behind it; all
+};
+RowsPlan rows_plan(const Layout &L, const CrossShape &s) {
+    RowsPlan p;
+    const size_t width = size_t(rows_shape(L, s, 1).max_blocks);
+    const size_t query = size_t(s.Hq) * (12 * size_t(L.d) + 8) + 4 * (width + 1);
+    size_t most = (size_t(1) << 27) / query;
+    if (most > size_t(65536 / s.Hq)) most = size_t(65536 / s.Hq);
+    if (most < 1) most = 1;
+    p.n = size_t(s.total_q) < most ? s.total_q : int(most);
+    // the last round has fewer rows, which may be split where the others' are not
+    const int rest = p.n ? s.total_q % p.n : 0;
+    p.inner = up256(attn_ws_bytes(L, rows_shape(L, s, p.n)));
+    if (rest) {
+        const size_t last = up256(attn_ws_bytes(L, rows_shape(L, s, rest)));
+        if (last > p.inner) p.inner = last;
+    }
+    p.lens = up256(4 * size_t(p.n));
+    p.total = p.inner + p.lens + up256(4 * size_t(p.n) * width);
+    return p;
+}
+
 }  // namespace
 
 // The size does not know the rotation of the parameters: it covers both ways.
 size_t cross_ws_bytes(const Layout &L, const CrossShape &s) {
-    const int n = queries_at_once(s);
-    const AttnShape r = rows_shape(L, s, n);
-    const size_t rows = up256(attn_ws_bytes(L, r)) + up256(4 * size_t(n)) + up256(4 * size_t(n) * size_t(r.max_blocks));
+    const size_t rows = rows_plan(L, s).total;
     if (!cross_tc_covers(L, false, s)) return rows;
     const size_t tc = cross_tc_ws_bytes(L, s);
     return tc > rows ? tc : rows;
@@ -88,9 +107,9 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
                  const uint8_t *cache, int64_t num_blocks, void *out, float *lse, uint8_t *ws, void *stream) {
     if (cross_tc_covers(L, kp->dev.rot || vp->dev.rot, s))
         return launch_cross_tc(kp, vp, L, Q, s, cache, num_blocks, out, lse, ws, static_cast<cudaStream_t>(stream));
-    const int n = queries_at_once(s);
+    const RowsPlan p = rows_plan(L, s);
+    const int n = p.n;
     AttnShape r = rows_shape(L, s, n);
-    const size_t inner = up256(attn_ws_bytes(L, r));
     CrossRows a;
     a.cu_q = s.cu_q;
     a.table = s.block_table;
@@ -101,8 +120,8 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
     a.max_kv_len = s.max_kv_len;
     a.P = L.P;
     a.width = r.max_blocks;
-    a.row_len = reinterpret_cast<int32_t *>(ws + inner);
-    a.row_table = reinterpret_cast<int32_t *>(ws + inner + up256(4 * size_t(n)));
+    a.row_len = reinterpret_cast<int32_t *>(ws + p.inner);
+    a.row_table = reinterpret_cast<int32_t *>(ws + p.inner + p.lens);
     a.status = reinterpret_cast<uint32_t *>(ws);
     r.seq_lens = a.row_len;
     r.block_table = a.row_table;
@@ -113,7 +132,7 @@ int launch_cross(const tq_params *kp, const tq_params *vp, const Layout &L, cons
         const int64_t at = int64_t(q0) * s.Hq;
         const int e = launch_attention(kp, vp, L, static_cast<const uint16_t *>(Q) + at * L.d, r, cache, num_blocks,
                                        static_cast<uint16_t *>(out) + at * L.d, lse ? lse + at : nullptr, nullptr, 0, ws,
-                                       inner, stream);
+                                       p.inner, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -153,3 +153,17 @@ def test_no_queries_and_no_sequences(codec):
     assert tqkv.cross_attn(kp, vp, desc, Q[:0], torch.zeros_like(cu), max_q, table, lens, most, cache).numel() == 0
     assert (tqkv.cross_attn(kp, vp, desc, Q, cu[:1], max_q, table[:0], lens[:0], most, cache) == 0).all()
     assert (tqkv.cross_attn(kp, vp, desc, Q, torch.zeros_like(cu), max_q, table, lens, most, cache) == 0).all()
+
+
+def test_rounds_of_long_table_rows():
+    """Room for 440,000 states in pages of 8: table rows of 220 KB, so some 600 queries a round by
+    rows; the last round has fewer rows and splits their keys."""
+    for total in (1150, 1200):
+        c = Call(Codec(*CODECS["d32"], P=8, H=1), [total - 5, 5], [300, 64], 1, extra_rows=3)
+        wide = torch.full((2, 55_000), -1, dtype=torch.int32, device=DEV)
+        wide[:, :c.table.shape[1]] = c.table
+        c.maxkv = 440_000
+        c.args = c.args[:6] + (wide, c.lens, c.maxkv, c.cache)
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check(out, lse, rows=[0, 1, 4, 590, 605, 606, 607, 608, 609, 610, 611, 612, total - 6])
