@@ -339,12 +339,16 @@ extern "C" size_t tq_pages_workspace_bytes(int64_t num_blocks, int n_rows, int m
 
 namespace {
 
+constexpr int kMostInts = INT32_MAX - 1024;
+
 bool pool_ok(const tq_cache_desc *desc, const tq_page_pool *p, void *ws, size_t ws_bytes) {
     if (!valid_desc(desc) || !p || !ws || !aligned(ws, 256)) return false;
     if (!p->refs || !p->table || !p->lens) return false;
     if (!aligned(p->refs, 4) || !aligned(p->table, 4) || !aligned(p->lens, 4)) return false;
     if (p->num_blocks < 1 || p->n_rows < 1 || p->max_blocks < 1) return false;
-    if (p->num_blocks > INT32_MAX / desc->page_tokens || p->max_blocks > INT32_MAX / desc->page_tokens) return false;
+    // the kernels' loops step past these counts by up to 1,024
+    if (p->num_blocks > kMostInts / desc->page_tokens || p->max_blocks > kMostInts / desc->page_tokens) return false;
+    if (p->n_rows > kMostInts) return false;
     return ws_bytes >= tq::pages_ws_bytes(p->num_blocks, p->n_rows, p->max_blocks);
 }
 
@@ -400,7 +404,7 @@ extern "C" int tq_pages_compact(const tq_cache_desc *desc, const tq_page_pool *p
 extern "C" int tq_pages_free(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *rows, int n,
                              void *workspace, size_t workspace_bytes, void *stream) {
     if (!pool_ok(desc, pool, workspace, workspace_bytes)) return TQ_EINVAL;
-    if (n < 0) return TQ_EINVAL;
+    if (n < 0 || n > kMostInts) return TQ_EINVAL;
     if (n == 0) return TQ_OK;
     if (!ints_ok(rows)) return TQ_EINVAL;
     tq::Layout L;
