@@ -358,7 +358,9 @@ int tq_cross_attn(const tq_params *kp, const tq_params *vp, const tq_cache_desc 
  * workspace's status word (TQ_DEV_BLOCK_RANGE: its row lists a page that is
  * out of range or free).  Entries of a table row behind its pages are never
  * read, and stay as they were.  num_blocks * page_tokens,
- * max_blocks * page_tokens, n_rows and n are below 2^31 - 1024.
+ * max_blocks * page_tokens, n_rows and n are below 2^31 - 1024.  The pool's
+ * arrays, the workspace and the requests (slot_mapping among them) do not
+ * overlap; src_rows and dst_rows may.
  * workspace: >= tq_pages_workspace_bytes(num_blocks, n_rows, max_blocks),
  * 256-byte aligned. */
 typedef struct {

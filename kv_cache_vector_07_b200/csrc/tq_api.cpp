@@ -1,6 +1,7 @@
 // C-ABI entry points of libtqkv: argument validation, workspace sizing and
 // dispatch to the kernel launchers.  See include/tqkv.h for the contract.
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -361,6 +362,31 @@ bool layers_ok(void *const *caches, int n_layers) {
 
 bool ints_ok(const int32_t *p) { return p && aligned(p, 4); }
 
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+bool apart(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes == 0 || b.bytes == 0 || (x <= y ? y - x >= a.bytes : x - y >= b.bytes);
+}
+// Whether the pool's arrays and the workspace, which a call writes, lie apart
+// from one another and from the requests: a kernel reads a request more than
+// once and goes by what it read first.
+bool requests_apart(const tq_page_pool *p, const void *ws, std::initializer_list<Span> requests) {
+    const Span own[4] = {{p->refs, 4 * size_t(p->num_blocks)},
+                         {p->table, 4 * size_t(p->n_rows) * size_t(p->max_blocks)},
+                         {p->lens, 4 * size_t(p->n_rows)},
+                         {ws, tq::pages_ws_bytes(p->num_blocks, p->n_rows, p->max_blocks)}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (!apart(own[i], own[j])) return false;
+        for (const Span &r : requests)
+            if (!apart(own[i], r)) return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" int tq_pages_reserve(const tq_cache_desc *desc, const tq_page_pool *pool, const int32_t *new_tokens,
@@ -368,6 +394,8 @@ extern "C" int tq_pages_reserve(const tq_cache_desc *desc, const tq_page_pool *p
                                 void *stream) {
     if (!pool_ok(desc, pool, workspace, workspace_bytes) || !ints_ok(new_tokens) || n_slots < 0) return TQ_EINVAL;
     if (n_slots > 0 && !ints_ok(slot_mapping)) return TQ_EINVAL;
+    const Span add{new_tokens, 4 * size_t(pool->n_rows)}, slots{slot_mapping, 4 * size_t(n_slots)};
+    if (!requests_apart(pool, workspace, {add, slots}) || !apart(add, slots)) return TQ_EINVAL;
     tq::Layout L;
     tq::make_layout(*desc, &L);
     return cuda_status(tq::launch_pages_reserve(L, *pool, new_tokens, slot_mapping, n_slots,
@@ -381,6 +409,7 @@ extern "C" int tq_pages_fork(const tq_cache_desc *desc, const tq_page_pool *pool
     if (n < 0 || n > pool->n_rows) return TQ_EINVAL;
     if (n == 0) return TQ_OK;
     if (!ints_ok(src_rows) || !ints_ok(dst_rows)) return TQ_EINVAL;
+    if (!requests_apart(pool, workspace, {{src_rows, 4 * size_t(n)}, {dst_rows, 4 * size_t(n)}})) return TQ_EINVAL;
     tq::Layout L;
     tq::make_layout(*desc, &L);
     return cuda_status(tq::launch_pages_fork(L, *pool, caches, n_layers, src_rows, dst_rows, n,
@@ -395,6 +424,9 @@ extern "C" int tq_pages_compact(const tq_cache_desc *desc, const tq_page_pool *p
     if (n < 0 || n > pool->n_rows || keep_stride < 0) return TQ_EINVAL;
     if (n == 0) return TQ_OK;
     if (!ints_ok(rows) || !ints_ok(keep_lens) || (keep_stride > 0 && !ints_ok(keep))) return TQ_EINVAL;
+    if (!requests_apart(pool, workspace, {{rows, 4 * size_t(n)}, {keep_lens, 4 * size_t(n)},
+                                          {keep, 4 * size_t(n) * size_t(keep_stride)}}))
+        return TQ_EINVAL;
     tq::Layout L;
     tq::make_layout(*desc, &L);
     return cuda_status(tq::launch_pages_compact(L, *pool, caches, n_layers, rows, keep, keep_stride, keep_lens, n,
@@ -406,7 +438,7 @@ extern "C" int tq_pages_free(const tq_cache_desc *desc, const tq_page_pool *pool
     if (!pool_ok(desc, pool, workspace, workspace_bytes)) return TQ_EINVAL;
     if (n < 0 || n > kMostInts) return TQ_EINVAL;
     if (n == 0) return TQ_OK;
-    if (!ints_ok(rows)) return TQ_EINVAL;
+    if (!ints_ok(rows) || !requests_apart(pool, workspace, {{rows, 4 * size_t(n)}})) return TQ_EINVAL;
     tq::Layout L;
     tq::make_layout(*desc, &L);
     return cuda_status(tq::launch_pages_free(L, *pool, rows, n, static_cast<uint8_t *>(workspace), stream));

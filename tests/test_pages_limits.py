@@ -14,3 +14,27 @@ TOP = 2 ** 31
     *[(name, dict(pool=dict(num_blocks=(TOP - 16) // 16), ws_bytes=1 << 60)) for name in ("reserve", "fork", "compact", "free")]])
 def test_counts_that_a_loop_would_step_past(name, kw):
     assert _c(name, **kw) == tqkv.TQ_EINVAL
+
+
+BASE = dict(refs=1 << 12, table=2 << 12, lens=3 << 12, num_blocks=10, n_rows=4, max_blocks=3)      # 40, 48 and 16 bytes
+
+
+def _calls(ints, ws=1 << 20, **pool):
+    """The codes of the four calls, every request at `ints`."""
+    kw = dict(pool=dict(BASE, **pool), ws=ws, ints=ints)
+    return [_c("reserve", **dict(kw, n_slots=0)), _c("fork", **kw), _c("compact", **dict(kw, keep=5 << 12)), _c("free", **kw)]
+
+
+@pytest.mark.parametrize("name", ["refs", "table", "lens"])
+def test_requests_within_the_pool(name):
+    size = dict(refs=40, table=48, lens=16)[name]
+    assert _calls(BASE[name]) == _calls(BASE[name] + size - 4) == [tqkv.TQ_EINVAL] * 4
+
+
+def test_arrays_that_overlap():
+    assert _calls(1 << 20) == _calls((1 << 20) + 256) == [tqkv.TQ_EINVAL] * 4                      # the workspace
+    assert _calls(4 << 12, ws=2 << 12) == [tqkv.TQ_EINVAL] * 4
+    assert _calls(4 << 12, lens=BASE["table"] + 44) == _calls(4 << 12, refs=BASE["lens"] - 36) == [tqkv.TQ_EINVAL] * 4
+    kw = dict(pool=BASE, ws=1 << 20, ints=4 << 12)
+    assert _c("reserve", **dict(kw, n_slots=9)) == tqkv.TQ_EINVAL                                   # new_tokens and slot_mapping
+    assert _c("compact", **dict(kw, keep=BASE["lens"] - 4, keep_stride=2)) == tqkv.TQ_EINVAL
