@@ -544,6 +544,8 @@ def _pool(desc, refs, table, lens, ints, workspace, stream, caches=None):
     if workspace is None:
         with _made_on(dev, stream):
             workspace = _workspace(pages_workspace_bytes(num_blocks, n_rows, max_blocks), refs.device)
+    elif not workspace.is_contiguous():                  # numel() is what it holds
+        raise ValueError("workspace must be contiguous")
     pool = _PagePool(refs.data_ptr(), table.data_ptr(), lens.data_ptr(), num_blocks, n_rows, max_blocks)
     return dev, pool, workspace, ptrs
 

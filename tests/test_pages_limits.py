@@ -38,3 +38,22 @@ def test_arrays_that_overlap():
     kw = dict(pool=BASE, ws=1 << 20, ints=4 << 12)
     assert _c("reserve", **dict(kw, n_slots=9)) == tqkv.TQ_EINVAL                                   # new_tokens and slot_mapping
     assert _c("compact", **dict(kw, keep=BASE["lens"] - 4, keep_stride=2)) == tqkv.TQ_EINVAL
+
+
+@pytest.mark.gpu
+def test_workspaces_that_are_not_what_they_count():
+    """A repeated byte counts as many as a workspace; a step of two is longer than it counts."""
+    import torch
+
+    from test_pages import DEV, Pair
+
+    p = Pair()
+    rows, need = p.ints([0]), p.ws.numel()
+    byte = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    for ws in (byte.expand(1 << 20), torch.zeros(2 * need, dtype=torch.uint8, device=DEV)[::2]):
+        for call in (lambda: tqkv.pages_free(p.desc, *p.state, rows, workspace=ws),
+                     lambda: tqkv.pages_fork(p.desc, p.caches, *p.state, rows, rows, workspace=ws),
+                     lambda: tqkv.pages_reserve(p.desc, *p.state, torch.zeros_like(p.state[2]), p.ints([0, 0]), workspace=ws),
+                     lambda: tqkv.pages_compact(p.desc, p.caches, *p.state, rows, p.ints([[0]]), rows, workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
