@@ -24,8 +24,10 @@
 // logarithm, the value's (2^e) on its offset, P' = 2^(l + e - m), while the sum
 // takes P' 2^-e.  The reference m follows l + e at a distance that keeps the
 // strongest weight of every tile between 2^-9 and 2^15: a weight is off by at
-// most 2^-11 of itself or 2^-25, the smallest step of fp16, which is 2^-16 of
-// its tile's strongest at worst and 2^-32 of the one that set m.
+// most 2^-11 of itself or 2^-25, half the smallest step of fp16, which is 2^-16
+// of its tile's strongest at worst and 2^-32 of the one that set m.  Keys whose
+// value is zero are left out of all this, however strong they are: their weights
+// go to the sum alone, in fp32.
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -41,11 +43,12 @@ namespace {
 constexpr int kTile = 128;                 // keys of a tile, and query rows of one
 
 // What the attention needs of a tile beside its operands.
-struct __align__(32) TileMeta {
+struct __align__(16) TileMeta {
     float kscale;                          // key = stored * kscale
     float vexp, vinv;                      // value = stored * 2^vexp; vinv = 2^-vexp
-    float unused;
-    uint32_t mask[4];                      // key k of the tile is there
+    uint32_t has_zero;                     // a bit of zero is set
+    uint32_t mask[4];                      // key k of the tile is there, and its value is not zero
+    uint32_t zero[4];                      // it is there, and its value is zero
 };
 
 constexpr size_t image_bytes(int d) { return size_t(kTile) * d * 2; }   // one operand tile
@@ -243,15 +246,11 @@ template <int D>
 constexpr size_t expand_smem() { return size_t(D) * D * 2 + 2 * image_bytes(D) + 1024; }
 
 // Power of two that brings mx to [2^(top - 1), 2^top); *e: value = stored * 2^e.
-// Zeros get an exponent below any other tile's (the smallest norm, 2^-24, times
-// the smallest largest level, 2^-4: -42): a tile without values then never sets
-// the reference that the other tiles' weights are relative to.  The factor ends
-// at 2^127: what is smaller than 2^(top - 128) (tiny queries) stays below 2^(top - 1).
-constexpr int kZeroExponent = -45;
+// The factor ends at 2^127: what is smaller than 2^(top - 128) (tiny queries)
+// stays below 2^(top - 1).
 __device__ __forceinline__ float scale_to(float mx, int top, int *e) {
     int ex = top;
-    if (mx == 0.f) ex = top + kZeroExponent;
-    else if (mx < INFINITY) frexpf(mx, &ex);
+    if (mx > 0.f && mx < INFINITY) frexpf(mx, &ex);
     ex = max(ex, top - 127);
     *e = ex - top;
     return ldexpf(1.f, top - ex);
@@ -293,6 +292,7 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
     __shared__ uint32_t tmem_holder;
     __shared__ __align__(8) uint64_t bar;
     __shared__ float red[2][2][8];
+    __shared__ uint32_t red_zero[2][8];
     __shared__ float lv[4][16], polar[2][132];
     __shared__ float bound[2];                        // of a coordinate over the vector's norm
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -458,9 +458,11 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         // a key's coordinate is below bound nk + rk sum_j |S_ji|, and |S_ji| below
         // 8.6 (Box-Muller of 53-bit uniforms)
         const float kmx = warp_max(fmaf(fabsf(rk), 8.6f * D, fabsf(nk) * bound[0])), vmx = warp_max(fabsf(nv) * bound[1]);
+        const uint32_t none = __ballot_sync(kFull, page && nv == 0.f);
         if (lane == 0) {
             red[0][phase & 1][warp] = kmx;
             red[1][phase & 1][warp] = vmx;
+            red_zero[phase & 1][warp] = none;
         }
         __syncthreads();
         float km = 0.f, vm = 0.f;
@@ -468,6 +470,12 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
         for (int i = 0; i < 8; ++i) {
             km = fmaxf(km, red[0][phase & 1][i]);
             vm = fmaxf(vm, red[1][phase & 1][i]);
+        }
+        if (tid == 0) {
+            uint32_t any = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= red_zero[phase & 1][i];   // the other warps have the same keys
+            a.meta[raw.at.image].has_zero = any;
         }
         int ek, ev;
         const float ksc = scale_to(km, 15, &ek), vsc = scale_to(vm, 15, &ev);
@@ -546,14 +554,16 @@ __global__ void __launch_bounds__(256, 2) cross_expand_kernel(const __grid_const
 #pragma unroll
             for (int c = 0; c < NC; ++c) *at(sK, c) = zero;
         }
-        const uint32_t there = __ballot_sync(kFull, page != nullptr);
+        const uint32_t there = __ballot_sync(kFull, page && nv != 0.f), zero_keys = __ballot_sync(kFull, page && nv == 0.f);
         TileMeta *m = a.meta + raw.at.image;
-        if (hh == 0 && lane == 0) m->mask[warp] = there;
+        if (hh == 0 && lane == 0) {
+            m->mask[warp] = there;
+            m->zero[warp] = zero_keys;
+        }
         if (tid == 0) {
             m->kscale = ldexpf(1.f, ek);
             m->vexp = float(ev);
             m->vinv = ldexpf(1.f, -ev);
-            m->unused = 0.f;
         }
         tc05::fence_proxy_async_smem();
         tc05::fence_before_sync();
@@ -610,7 +620,7 @@ __device__ __forceinline__ int64_t part_tile(const AttendArgs &a, int split, int
     return (((int64_t(split) * gridDim.y + pl) * a.x) + x) * 2 + tt;
 }
 
-// (m + log2 l) ln 2.  l may be 2^50 and m as far below zero (tiles of zeros), so
+// (m + log2 l) ln 2.  l may be 2^100 and m as far below zero (zero values), so
 // l's exponent is taken to m before the rest, which is in [-1, 0), is added.
 __device__ __forceinline__ float lse_of(float m, float l) {
     int e;
@@ -642,6 +652,51 @@ __device__ __forceinline__ void sign_regs(float2 (&x)[D / 2], const float *signs
         x[2 * i] = mul2(x[2 * i], make_float2(s.x, s.y));
         x[2 * i + 1] = mul2(x[2 * i + 1], make_float2(s.z, s.w));
     }
+}
+
+// The keys of value zero of a tile go to the sum alone: zs 2^zm in all, in units
+// of 2^m.  They count as values of 2^-86 where that is above the reference, so
+// that the sum stays below 2^127.  Returns m and l as they are then; has_o: there
+// is an O to follow m.  Read from tensor memory again, before the loop's own 128
+// registers of S are filled: asking for it costs every tile 1 % (8 runs of 1,024
+// over up to 8,192 states, attention 408 -> 412 us), done on those registers 5 %.
+template <int D>
+__device__ __noinline__ float2 zero_keys(uint32_t ts, uint32_t to, const TileMeta *meta, float c2, float m, float l,
+                                         bool has_o) {
+    float zs = 0.f, zm = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t bits = meta->zero[c];
+        if (bits == 0u) continue;
+        float v[32], top = zm, part = 0.f;
+        tc05::tmem_ld_32x32b_x32(ts + uint32_t(c * 32), reinterpret_cast<uint32_t(&)[32]>(v));
+        tc05::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if ((bits >> e) & 1u) top = fmaxf(top, v[e]);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if ((bits >> e) & 1u) part += ex2_approx((v[e] - top) * c2);
+        zs = fmaf(zs, ex2_approx((zm - top) * c2), part);
+        zm = top;
+    }
+    zm *= c2;
+    const bool up = zm - 86.f - m > 15.f;
+    const float ref = up ? ceilf(zm) - 93.f : m, alpha = up ? exp2f(m - ref) : 1.f;
+    l = fmaf(l, alpha, zs * exp2f(zm - ref));
+    if (has_o && __any_sync(kFull, up)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc05::tmem_ld_32x32b_x32(to + uint32_t(c * 32), o);
+            tc05::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc05::tmem_st_32x32b_x32(to + uint32_t(c * 32), o);
+        }
+        tc05::tmem_wait_st();
+    }
+    return make_float2(ref, l);
 }
 
 template <int D>
@@ -926,13 +981,22 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
         };
         float m = -INFINITY, l = 0.f;                      // log2 units
         for (int j = 0; j < n; ++j) {
-            if (!wait_w(&meta_full[j % kMetaSlots], uint32_t(j / kMetaSlots) & 1u) ||
-                !wait_w(&s_full[tt], uint32_t(j) & 1u)) {
+            if (!wait_w(&meta_full[j % kMetaSlots], uint32_t(j / kMetaSlots) & 1u)) {
+                timeout = true;
+                break;
+            }
+            const float4 sc = *reinterpret_cast<const float4 *>(&smeta[j % kMetaSlots]);
+            if (!wait_w(&s_full[tt], uint32_t(j) & 1u)) {
                 timeout = true;
                 break;
             }
             tc05::fence_after_sync();
-            const float4 sc = *reinterpret_cast<const float4 *>(&smeta[j % kMetaSlots]);
+            const float c2 = fmaxf(rowc * sc.x, 1e-37f);
+            if (__float_as_uint(sc.w) != 0u) {
+                const float2 ml = zero_keys<D>(ts, to, smeta + j % kMetaSlots, c2, m, l, j > 0);
+                m = ml.x;
+                l = ml.y;
+            }
             const uint4 mask = *reinterpret_cast<const uint4 *>(smeta[j % kMetaSlots].mask);
             float s[128];
 #pragma unroll
@@ -953,7 +1017,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
 #pragma unroll
             for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(mx4[u], s[124 + u]);
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            const float c2 = fmaxf(rowc * sc.x, 1e-37f);
             const float top = fmaf(mx, c2, sc.y);
             // Set to 2^7 below the strongest weight, the reference moves only
             // when a tile's strongest leaves [2^-9, 2^15], so O is rescaled a
@@ -963,9 +1026,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             // the sum is below 2^60, and stay below 2^106.
             const float d = top - m;
             const bool move = d > 15.f || (d < -9.f && d > -1e30f && l < 0x1p60f);
-            const float ref = fmaxf(top - 7.f, m - 30.f);
-            const float alpha = move ? exp2f(m - ref) : 1.f;
+            float alpha = 1.f;
             if (move) {
+                const float ref = fmaxf(ceilf(top) - 7.f, m - 30.f);   // whole numbers: factors are exact
+                alpha = exp2f(m - ref);
                 m = ref;
                 l *= alpha;
             }

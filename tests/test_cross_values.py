@@ -13,7 +13,7 @@ import pytest
 import torch
 
 from kv_cache_vector_07_b200 import synth, tqkv
-from test_cross import CODECS, DEV, Call, Codec
+from test_cross import CODECS, DEV, Call, Codec, U
 
 pytestmark = pytest.mark.gpu
 
@@ -43,6 +43,20 @@ class Made(Call):
                         torch.from_numpy(slots).to(DEV), self.cache)
         noise = torch.randn(self.Q.shape, generator=g, dtype=torch.float64)
         self.Q.copy_(math.sqrt(d) * u + 0.3 * noise)
+        # A logit of size l is a sum of products that go as u_i^2, each off by two fp16 roundings (rms
+        # 2^-11 / sqrt 3 of it at most), so by l 2^-11 sqrt(2/3 sum u_i^4), and the query's half of that
+        # is the same for every key of a row: it does not average out in the 2-norm (1.2 times that here).
+        self.share = below * math.log(2) * U * math.sqrt(float((u ** 4).sum()))
+
+    def check_far(self, out, lse):
+        """check where logits are large: 2^-8 and the share above for the 2-norm."""
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        err2 = ref2 = 0.0
+        for pick, hs, ref, rl, tol, tl in self.reference():
+            e, f = np.abs(o[pick, hs].reshape(ref.shape) - ref), np.abs(l[pick, hs].reshape(-1) - rl)
+            assert (e <= tol).all() and (f <= tl).all(), ((e / tol).max(), (f / tl).max())
+            err2, ref2 = err2 + (e ** 2).sum(), ref2 + (ref ** 2).sum()
+        assert err2 <= (2.0 ** -8 + self.share) ** 2 * ref2, math.sqrt(err2 / ref2)
 
 
 def constant(norm):
@@ -167,3 +181,15 @@ def test_rounds_of_long_table_rows():
         out, lse, flags = c.run()
         assert flags == 0
         c.check(out, lse, rows=[0, 1, 4, 590, 605, 606, 607, 608, 609, 610, 611, 612, total - 6])
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64", "33"])
+@pytest.mark.parametrize("length", [70, 130, 1500, 4096])
+@pytest.mark.parametrize("below", [30, 60, 75])
+def test_strong_keys_without_a_value_far_above(codec, length, below):
+    """Their neighbours' weights alone make the result: keys 7, 707, 1407 and so on have no value."""
+    for norm in (11.0, 0.003):
+        c = Made(codec_of(codec, 1), [70, 7], [length, 70], 4, lambda t, n: t % 700 == 7, below, constant(norm))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check_far(out, lse)
