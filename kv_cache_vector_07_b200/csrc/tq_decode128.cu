@@ -165,6 +165,13 @@ __device__ __forceinline__ T lds_at(const void *base, uint32_t byte_off) {
     return *reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(base) + byte_off);
 }
 
+// Blocks an SM that CROSS kernels leave registers for: as many as the decode
+// step's have (32 rows x 32 heads over up to 2,048 states, 2-bit keys: 61.2 us a
+// call with five, 64.0 with the four that 100 registers leave); fractional and
+// polar codes of more than four heads would spill for it (95.6 against 96.6 us).
+template <int KB, int NT, bool FR, bool PL>
+__host__ __device__ constexpr int cross_blocks() { return KB == 2 && !FR && !PL ? 5 : (FR || PL) && NT == 2 ? 1 : 4; }
+
 // Polar codes (PL, keys with QJL and values, d = 128): the unit-radius
 // reconstruction is rebuilt per token in registers, top down through the
 // angle tree (each radius the parent's times the cos / sin of the parent's
@@ -172,8 +179,16 @@ __device__ __forceinline__ T lds_at(const void *base, uint32_t byte_off) {
 // fp16 hi + lo pairs are the MMA operands.  Keys as for 4-bit codes (thread
 // t: pairs 16t .. 16t + 15), values as for 4-bit codes (thread g: pairs
 // 8g .. 8g + 7); no pair tables, two 132-float angle tables.
-template <int KB, int VB, int NT, bool FR = false, bool PL = false>
-__global__ void __launch_bounds__(128) dec128_kernel(Dec128Args a) {
+//
+// CROSS (rows of cross attention): P' takes the value's norm into fp16, so a
+// weight's reference is the largest l + log2(norm) of the row, 2^14 below the
+// largest P', not the largest l: weights keep 11 bits down to 2^-28 of the
+// strongest contribution, whatever the values' size and however strong a key
+// without a value is (by the largest l, one key of value zero above 1,500
+// others cost 0.3 % of the result at 2^20 and 4 % at 2^24; with values of norm
+// 0.003 7 % at 2^16).
+template <int KB, int VB, int NT, bool FR = false, bool PL = false, bool CROSS = false>
+__global__ void __launch_bounds__(128, CROSS ? cross_blocks<KB, NT, FR, PL>() : 1) dec128_kernel(Dec128Args a) {
     static_assert(KB == 2 || KB == 4 || KB == 8 || (FR && KB == 3), "key bits");
     static_assert(VB == 3 || VB == 4, "value bits");
     static_assert(!FR || ((KB == 2 || KB == 3) && VB == 4), "fractional rates: keys 1.5 / 2.5 bits, values 3.5");
@@ -641,6 +656,13 @@ __global__ void __launch_bounds__(128) dec128_kernel(Dec128Args a) {
             const float nv0 = h2f_bits(*reinterpret_cast<const uint16_t *>(pg + L.vn_off + (pr + g) * 2));
             const float nv1 = h2f_bits(*reinterpret_cast<const uint16_t *>(pg + L.vn_off + (pr + g + 8) * 2));
             const bool ok0 = tok0 + g < nv, ok1 = tok0 + g + 8 < nv;
+            // CROSS: log2 of the norms.  A value that is zero counts as 2^-86: its
+            // weight, at most 2^100 of the reference, stays within the fp32 sum
+            float lg0 = 0.f, lg1 = 0.f;
+            if constexpr (CROSS) {
+                lg0 = fmaxf(__log2f(nv0), -86.f);
+                lg1 = fmaxf(__log2f(nv1), -86.f);
+            }
             // ---------------- online softmax (log2 units) for heads t and 4 + t
             uint32_t pk[NT];           // half2(P'[token g][h], P'[token g+8][h])
             uint32_t pk_lo = 0;        // one head tile: P' - fp16(P') for the spare columns
@@ -655,10 +677,11 @@ __global__ void __launch_bounds__(128) dec128_kernel(Dec128Args a) {
                     if (ok0) a.logits[(row0 + hd) * a.logits_stride + tok0 + g] = l0 * inv_l2e;
                     if (ok1) a.logits[(row0 + hd) * a.logits_stride + tok0 + g + 8] = l1 * inv_l2e;
                 }
-                float mx = fmaxf(l0, l1);
+                float mx = CROSS ? fmaxf(l0 + lg0, l1 + lg1) : fmaxf(l0, l1);
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                if (CROSS) mx = ceilf(mx) - 14.f;       // a whole number: factors between references are exact
                 const float m_new = fmaxf(m_run[nt], mx);
                 const float al = m_new == -INFINITY ? 1.f : exp2f(m_run[nt] - m_new);
                 const float p0 = m_new == -INFINITY ? 0.f : exp2f(l0 - m_new);
@@ -932,12 +955,34 @@ __global__ void __launch_bounds__(128) dec128_kernel(Dec128Args a) {
     }
     __syncthreads();
     const int64_t pbase = (int64_t(grp) * a.n_splits + split) * G;
+    if constexpr (CROSS) {
+        // the sum may be 2^100 and the reference as far below the logits: the
+        // sum's exponent goes to the reference, so that their logarithms add up
+        // without losing digits
+        if (tid < G) {
+            float M = -INFINITY;
+            for (int w2 = 0; w2 < 4; ++w2) M = fmaxf(M, mm[w2 * 8 + tid]);
+            float S = 0.f;
+            for (int w2 = 0; w2 < 4; ++w2) {
+                const float mw = mm[w2 * 8 + tid];
+                if (mw != -INFINITY) S += ll[w2 * 8 + tid] * exp2f(mw - M);
+            }
+            int k = 0;
+            if (S > 0.f && S < INFINITY) frexpf(S, &k);
+            const float down = ldexpf(1.f, -k);
+            mm[tid] = down;                                      // read by this thread alone, and that above
+            a.part_ml[(pbase + tid) * 2] = M == -INFINITY ? -INFINITY : (M + float(k)) * 0.6931471805599453f;
+            a.part_ml[(pbase + tid) * 2 + 1] = S * down;
+        }
+        __syncthreads();
+    }
     for (int i = tid; i < G * 128; i += 128) {
         float o = ((oo[i] + oo[1024 + i]) + oo[2048 + i]) + oo[3072 + i];
         if (NT == 1) o += ((oo[512 + i] + oo[1536 + i]) + oo[2560 + i]) + oo[3584 + i];
+        if (CROSS) o *= mm[i >> 7];
         a.part_o[pbase * 128 + i] = o;
     }
-    if (tid < G) {
+    if (!CROSS && tid < G) {
         float M = -INFINITY;
         for (int w2 = 0; w2 < 4; ++w2) M = fmaxf(M, mm[w2 * 8 + tid]);
         float S = 0.f;
@@ -986,7 +1031,8 @@ int dec_resident(int page_bytes) {
 template <int KB, int VB, int NT, bool FR = false, bool PL = false>
 int run_dec(const Dec128Args &a, int n_groups, cudaStream_t st) {
     const size_t smem = dec_smem<KB, VB, NT, FR, PL>(a.L.page_bytes);
-    auto kern = dec128_kernel<KB, VB, NT, FR, PL>;
+    // chained: rows of cross attention
+    auto kern = a.chained ? dec128_kernel<KB, VB, NT, FR, PL, true> : dec128_kernel<KB, VB, NT, FR, PL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const dim3 grid{unsigned(n_groups), unsigned(a.n_splits)};

@@ -193,3 +193,34 @@ def test_strong_keys_without_a_value_far_above(codec, length, below):
         out, lse, flags = c.run()
         assert flags == 0
         c.check_far(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "k3v4", "k8v4", "frac", "polar", "33", "d32"])
+@pytest.mark.parametrize("G", [4, 7])
+def test_strong_keys_without_a_value_by_rows(codec, G):
+    """Runs of a few queries: weights far below a key that has none of the result, values of any size."""
+    cd = codec_of(codec, 1)
+    for below, norm, length in ((16, 0.003, 1500), (20, 11.0, 1500), (24, 1.0, 4096), (30, 0.02, 130), (60, 1.0, 1500)):
+        c = Made(cd, [2, 1], [length, 70], G, lambda t, n: t % 700 == 7, below, constant(norm))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check_far(out, lse)
+
+
+def test_strong_keys_without_a_value_under_the_dense_rotation():
+    cd = Codec(128, 4, True, 4, H=1, dense=True)
+    for qlens in ([2, 1], [20, 9]):
+        c = Made(cd, qlens, [1500, 70], 4, lambda t, n: t % 700 == 7, 24, constant(0.01))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check_far(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "k3v4", "d64", "d32"])
+@pytest.mark.parametrize("norm", [2.0 ** -13, 4000.0])
+def test_small_and_large_values(codec, norm):
+    for qlens in ([2, 3], [70, 9]):
+        c = Made(codec_of(codec, 2), qlens, [900, 64], 2, lambda t, n: t < 0, 0, constant(norm))
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check(out, lse)
