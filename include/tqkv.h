@@ -331,7 +331,11 @@ int tq_score(const tq_params *p, const tq_cache_desc *desc, const void *db_cache
  * NaN in its own row and head.  Rows of Q behind cu_q[B], and queries behind a
  * run's first max_q (TQ_DEV_ROW), are neither read nor written.  kv_lens above
  * max_kv_len count as max_kv_len.  Keys of a page out of range are left out
- * (TQ_DEV_BLOCK_RANGE).
+ * (TQ_DEV_BLOCK_RANGE).  A weight counts by what it adds to the result: keys
+ * whose value is zero may stand up to 2^86 above the others without costing the
+ * result bits.  Logits are below 2^24 in size, the coordinates of R q and S R q
+ * below 2^18; beyond that the result is not defined (no page or row is read or
+ * written that would not be otherwise).
  * workspace: >= tq_cross_workspace_bytes(desc, B, total_q, max_q, Hq,
  * max_kv_len), 256-byte aligned. */
 size_t tq_cross_workspace_bytes(const tq_cache_desc *desc, int B, int total_q, int max_q, int Hq, int max_kv_len);

@@ -9,7 +9,7 @@
 // pages once for each.  Right for every codec, rotation and head size; what it
 // reads grows with the run, so it serves runs of a few queries and what the
 // tensor-core way does not cover.  32 rows x 32 heads over up to 2,048 tokens of
-// k3v4: 4 us for the rows, 10 to prepare the queries, 47 to read, 8 to join; the
+// k3v4: 4 us for the rows, 10 to prepare the queries, 49 to read, 8 to join; the
 // bytes alone are 7.
 #include <cuda_runtime.h>
 
