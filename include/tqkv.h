@@ -332,7 +332,7 @@ int tq_score(const tq_params *p, const tq_cache_desc *desc, const void *db_cache
  * run's first max_q (TQ_DEV_ROW), are neither read nor written.  kv_lens above
  * max_kv_len count as max_kv_len.  Keys of a page out of range are left out
  * (TQ_DEV_BLOCK_RANGE).  A weight counts by what it adds to the result: keys
- * whose value is zero may stand up to 2^86 above the others without costing the
+ * whose value is zero may stand up to 2^64 above the others without costing the
  * result bits.  Logits are below 2^24 in size, the coordinates of R q and S R q
  * below 2^18; beyond that the result is not defined (no page or row is read or
  * written that would not be otherwise).

@@ -1023,9 +1023,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             // few times a row, not every tile.  It moves down, too: where one
             // strong key has a small value, the result is made of the others'
             // weights.  O and the sum, fp32, grow by 2^30 at most a time while
-            // the sum is below 2^60, and stay below 2^106.
+            // the sum is below 2^72: O, at most 2^16 times the sum, stays below 2^118.
             const float d = top - m;
-            const bool move = d > 15.f || (d < -9.f && d > -1e30f && l < 0x1p60f);
+            const bool move = d > 15.f || (d < -9.f && d > -1e30f && l < 0x1p72f);
             float alpha = 1.f;
             if (move) {
                 const float ref = fmaxf(ceilf(top) - 7.f, m - 30.f);   // whole numbers: factors are exact

@@ -224,3 +224,15 @@ def test_small_and_large_values(codec, norm):
         out, lse, flags = c.run()
         assert flags == 0
         c.check(out, lse)
+
+
+@pytest.mark.parametrize("codec", ["k5v4", "d64", "d32"])
+@pytest.mark.parametrize("qlens", [[2, 1], [70, 9]])
+def test_weights_at_the_end_of_the_stated_range(codec, qlens):
+    """Keys without a value 2^64 above the others, whose values are small, and change size from tile to tile."""
+    steps = np.array([-13, -9, -3, -13])
+    for length in (1024, 3000):
+        c = Made(codec_of(codec, 1), qlens, [length, 70], 2, lambda t, n: t % 300 == 7, 64, lambda t: 2.0 ** steps[t // 128 % 4])
+        out, lse, flags = c.run()
+        assert flags == 0
+        c.check_far(out, lse)
