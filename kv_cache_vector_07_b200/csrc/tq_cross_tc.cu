@@ -1026,10 +1026,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) cross_attend_kernel(const _
             // the sum is below 2^72: O, at most 2^16 times the sum, stays below 2^118.
             const float d = top - m;
             const bool move = d > 15.f || (d < -9.f && d > -1e30f && l < 0x1p72f);
-            float alpha = 1.f;
+            const float ref = fmaxf(ceilf(top) - 7.f, m - 30.f);   // whole numbers: factors are exact
+            const float alpha = move ? exp2f(m - ref) : 1.f;
             if (move) {
-                const float ref = fmaxf(ceilf(top) - 7.f, m - 30.f);   // whole numbers: factors are exact
-                alpha = exp2f(m - ref);
                 m = ref;
                 l *= alpha;
             }
